@@ -10,9 +10,11 @@ Entry points (same names as the C ABI in include/fp4lin.h):
   nvfp4_quantize, nvfp4_gemm, mxfp4_quantize, mxfp4_gemm,
   kv_nvfp4_store, kv_nvfp4_load_fp8, kv_nvfp4_attention, nvfp4_gemm_quant,
   nvfp4_linear_decode, nvfp4_gemm_tiled, gptq_quantize
+and, of include/fp4lin_serving.h (serving.py):
+  rmsnorm_mxfp8, nvfp4_matvec, mxfp4_matvec, kv_block_tables, kv_fp8_store, kv_fp8_attention
 plus helpers: scale_bytes, gemm_workspace_bytes, tile_weights, device_status,
 convert_selftest, wait_selftest, prepare_weight, prepare_weight_gptq,
-gptq_hessian_factor, nvfp4_linear, mxfp4_linear.
+gptq_hessian_factor, nvfp4_linear, mxfp4_linear, weight_only_linear.
 
 Errors: a caller-supplied tensor of the wrong dtype raises TypeError; one in host
 memory, on another device, in a layout the call cannot take, or smaller than the
@@ -30,13 +32,16 @@ from dataclasses import dataclass
 import torch
 
 from . import build as _build
+from .serving import (SERVING_EXPORTS, kv_block_tables, kv_fp8_attention, kv_fp8_store, mxfp4_matvec, nvfp4_matvec,
+                      rmsnorm_mxfp8, weight_only_linear)
 
 __all__ = [
     "Fp4LinError", "lib", "nvfp4_quantize", "nvfp4_gemm", "mxfp4_quantize", "mxfp4_gemm",
     "kv_nvfp4_store", "kv_nvfp4_load_fp8", "scale_bytes", "gemm_workspace_bytes",
     "device_status", "convert_selftest", "wait_selftest", "QuantizedWeight", "prepare_weight", "nvfp4_linear",
     "mxfp4_linear", "nvfp4_linear_decode", "tile_weights", "nvfp4_gemm_tiled", "gptq_quantize", "gptq_hessian_factor", "prepare_weight_gptq",
-    "EXPORTS",
+    "rmsnorm_mxfp8", "nvfp4_matvec", "mxfp4_matvec", "weight_only_linear", "kv_block_tables", "kv_fp8_store",
+    "kv_fp8_attention", "EXPORTS", "SERVING_EXPORTS",
 ]
 
 STATUS = {0: "OK", 1: "INVALID_ARGUMENT", 2: "UNSUPPORTED_SHAPE", 3: "MISALIGNED", 4: "CUDA",
@@ -98,7 +103,7 @@ def lib() -> ctypes.CDLL:
         if _lib is None:
             path = _build.build()
             L = ctypes.CDLL(path)
-            for name, (res, args) in EXPORTS.items():
+            for name, (res, args) in (EXPORTS | SERVING_EXPORTS).items():
                 fn = getattr(L, name)
                 fn.restype, fn.argtypes = res, args
             _lib = L

@@ -1541,3 +1541,5 @@ int gptq_hessian_factor(const double *x, int64_t T, int64_t K, int64_t ld_x, int
 }
 
 }  // extern "C"
+
+#include "serving_abi.cuh"

@@ -1,0 +1,437 @@
+// kv_paged_attention.cuh -- causal attention of a ragged batch's new tokens over the paged 8-bit
+// cache (kv_paged.cuh): request b has len_b rows in the cache before this step and n_b = cu[b+1] -
+// cu[b] new tokens whose rows are in it too; new token i sees positions 0 .. len_b + i.  Query head
+// j uses kv head j / G.  With codes k, v and page exponents Xk, Xv:
+//   s_l = scale * 2^Xk * (q . k_l),  o = sum_l softmax(s)_l * 2^Xv * v_l.
+//
+// The value scale rides in the exponent: with s'_l = log2(e) s_l + Xv(l) and M = max s',
+//   w_l = 2^(s'_l - M),  o = (sum_l w_l v_l) / (sum_l w_l 2^-Xv(l)),
+// so one running maximum and one exponential a score serve both sums, the weights that meet the
+// value codes are at most 1 whatever the pages' scales, and one fused multiply-add applies both
+// scales.  A page whose value byte is 0 (all codes zero) takes part in the second sum only; it uses
+// the exponent of KVP_ZERO_X there, so that it does not move M far.
+// Scores, maxima, sums and outputs are binary32.  K and V codes are exact in f16; q is scaled by a
+// power of two to [1, 2) at its row's maximum (exact down to 2^-14 of it); the weights are rounded
+// to f16 (2^-11 each, against bf16 outputs).
+#pragma once
+
+#include "gemm_sm100.cuh"
+#include "kv_attention.cuh"  // mma_16816x, f16x2_bits
+#include "mxfp8.cuh"
+
+namespace fp4lin {
+
+constexpr int KVP_THREADS = 128;
+constexpr int KVP_WARPS = KVP_THREADS / 32;
+constexpr int KVP_MAX_CHUNK = 2048;    // keys a CTA
+constexpr int KVP_STEP = 32;           // keys a warp takes at a time
+constexpr float KVP_ZERO_X = -8.0f;
+
+struct KvPagedShape {
+    const __nv_bfloat16 *q;  // [T, H*G, D], token stride ld_q
+    const uint8_t *kc, *ks, *vc, *vs;
+    const int32_t *table, *lens, *cu;
+    __nv_bfloat16 *out;      // [T, H*G, D]
+    float *ws;               // [B*H, tiles, S, rows, D + 2]
+    int64_t ld_q, ld_t;
+    float qscale;            // scale * log2(e)
+    int B, H, G, T, NP, shift, max_new, max_len;
+    int chunk, S, tiles;
+};
+
+// One request as a CTA sees it; ok is false where the lengths cannot be what the caller promised
+// (the request is skipped and reported).
+struct KvPagedRequest {
+    int len, first, n;
+    bool ok;
+};
+
+__device__ __forceinline__ KvPagedRequest kvp_request(const KvPagedShape &a, int b)
+{
+    KvPagedRequest r;
+    r.len = a.lens[b];
+    r.first = a.cu[b];
+    const int64_t n = (int64_t)a.cu[b + 1] - r.first;
+    r.ok = r.len >= 0 && r.first >= 0 && n >= 0 && n <= a.max_new && r.first + n <= a.T &&
+           (int64_t)r.len + n <= a.max_len;
+    r.n = r.ok ? (int)n : 0;
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Transpose of an 8 x 8 f16 fragment.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Row `rho` of a tile as f16 B fragments: this lane's D/4 values (d = t*D/4 ..) in the order the
+// key codes are used, scaled by 2^-e with e the row's largest exponent.  Returns 2^e (0 rows: 1).
+template <int D>
+__device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, uint32_t (*qb)[2])
+{
+    uint4 u[D / 32];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        u[i] = live ? ld_nc_v4(p + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        float f[8];
+        bf16x8_to_f32(u[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = fmaxf(m, finite_abs(f[j]));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // exponent byte of m, kept where both 2^e and 2^-e are normal
+    const uint32_t e = m > 0.0f ? min(max(__float_as_uint(m) >> 23, 1u), 253u) : 127u;
+    const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        bf16x8_to_f32(u[i], f);
+        qb[2 * i][0] = f16x2_bits(f[0] * inv, f[1] * inv);
+        qb[2 * i][1] = f16x2_bits(f[2] * inv, f[3] * inv);
+        qb[2 * i + 1][0] = f16x2_bits(f[4] * inv, f[5] * inv);
+        qb[2 * i + 1][1] = f16x2_bits(f[6] * inv, f[7] * inv);
+    }
+    return __uint_as_float(e << 23);
+}
+
+// Split form: CTA (s, b*H + h, z) takes keys [s*chunk, (s+1)*chunk) for rows z*8*NT .. of the
+// request's n*G (token, head) rows.  HBM bound for single tokens: every K and V byte is loaded once,
+// straight into registers as tensor-core fragments -- no shared memory, no exchange between warps
+// until the end.  A warp takes 32 keys at a time (its next K and V rows are in flight while it works).
+// Scores^T = K q^T by mma_16816x (A: 16 keys x 16 dimensions, B: 8 rows of q): a lane needs rows
+// g and g+8 of the keys, whichever dimensions, as long as q uses the same: it takes D/4 contiguous
+// bytes.  O^T += V^T w^T: the lane needs the same dimension of keys 2t, 2t+1 in one register, two
+// byte permutes of two rows' words; it takes D/8 contiguous dimensions (those of all D/16 M tiles).
+// The weights change from the score layout to B fragments by an 8 x 8 transpose in registers.
+template <int D, int NT>
+__global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShape a)
+{
+    constexpr int R = 8 * NT, KW = D / 16, VW = D / 32;  // rows, 32-bit words a lane needs of a K / V row
+    __shared__ int s_page[KVP_MAX_CHUNK / 16];
+    __shared__ float s_kf[KVP_MAX_CHUNK / 16], s_xv[KVP_MAX_CHUNK / 16];
+    __shared__ float s_m[KVP_WARPS][R], s_den[KVP_WARPS][R];
+    __shared__ float s_o[KVP_WARPS][R][D + 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
+    pdl_wait();
+    const KvPagedRequest rq = kvp_request(a, b);
+    if (!rq.ok && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0)
+        report_error(FP4LIN_ERR_OUT_OF_RANGE);
+    const int rows = rq.n * a.G, row0 = blockIdx.z * R;
+    if (row0 >= rows)
+        return;
+    const int imin = row0 / a.G, imax = (min(row0 + R, rows) - 1) / a.G;
+    const int k0 = blockIdx.x * a.chunk, kend = rq.len + imax + 1;  // keys the tile's last row sees
+    if (k0 >= kend)
+        return;
+    const int k1 = min(kend, k0 + a.chunk), held = rq.len + rq.n;  // rows behind `held` hold anything
+    const int P1 = (1 << a.shift) - 1;
+
+    for (int i = tid; i < (k1 - k0 + 15) / 16; i += KVP_THREADS) {
+        const int page = a.table[b * a.ld_t + ((k0 + 16 * i) >> a.shift)];
+        const bool ok = page >= 0 && page < a.NP;
+        if (!ok)
+            report_error(FP4LIN_ERR_OUT_OF_RANGE);
+        const uint32_t kb = ok ? a.ks[(int64_t)page * a.H + h] : 0u, vb = ok ? a.vs[(int64_t)page * a.H + h] : 0u;
+        s_page[i] = ok ? page : -1;
+        s_kf[i] = mxfp8_scale(kb);
+        s_xv[i] = ok ? (vb ? (float)((int)vb - 127) : KVP_ZERO_X) : -INFINITY;  // no page: weight 0
+    }
+    uint32_t qb[NT][KW][2];
+    float qs[NT][2];
+    int lim[NT][2];  // last key that this lane's rows (columns 2t, 2t+1 of the scores) see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int rho = row0 + 8 * nt + g, i = rho / a.G, j = rho - i * a.G;
+        const bool live = rho < rows;
+        const float s = kvp_load_q<D>(a.q + (int64_t)(rq.first + (live ? i : 0)) * a.ld_q + (h * a.G + (live ? j : 0)) * D +
+                                          t * (D / 4),
+                                      live, qb[nt]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            qs[nt][c] = __shfl_sync(0xffffffffu, s, (2 * t + c) * 4) * a.qscale;
+            const int r = row0 + 8 * nt + 2 * t + c;
+            lim[nt][c] = r < rows ? rq.len + r / a.G : -1;
+        }
+    }
+    __syncthreads();
+
+    uint32_t kr[2][2][KW], vr[2][4][VW];
+    auto row_ptr = [&](const uint8_t *codes, int key) {  // row `key` of this head; null where there is none
+        const int page = s_page[(key - k0) >> 4];
+        return page < 0 ? nullptr : codes + (((int64_t)page * a.H + h) << a.shift) * D + (int64_t)(key & P1) * D;
+    };
+    auto load_k = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = kb + 16 * u + 8 * e + g;
+                const uint8_t *p = key < k1 ? row_ptr(a.kc, key) : nullptr;
+#pragma unroll
+                for (int w = 0; w < KW; w += 4) {
+                    const uint4 x = p ? ld_nc_v4(p + t * (D / 4) + 4 * w) : make_uint4(0u, 0u, 0u, 0u);
+                    kr[u][e][w] = x.x;
+                    kr[u][e][w + 1] = x.y;
+                    kr[u][e][w + 2] = x.z;
+                    kr[u][e][w + 3] = x.w;
+                }
+            }
+    };
+    auto load_v = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = kb + 16 * u + 2 * t + (e & 1) + 8 * (e >> 1);
+                const uint8_t *p = key < k1 && key < held ? row_ptr(a.vc, key) : nullptr;
+                if constexpr (VW == 4) {
+                    const uint4 x = p ? ld_nc_v4(p + g * 16) : make_uint4(0u, 0u, 0u, 0u);
+                    vr[u][e][0] = x.x;
+                    vr[u][e][1] = x.y;
+                    vr[u][e][2] = x.z;
+                    vr[u][e][3] = x.w;
+                } else {
+                    const uint2 x = p ? ld_nc_v2(p + g * 8) : make_uint2(0u, 0u);
+                    vr[u][e][0] = x.x;
+                    vr[u][e][1] = x.y;
+                }
+            }
+    };
+
+    float o[NT][D / 16][4], den[NT][2], M[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        M[nt][0] = M[nt][1] = -INFINITY;
+        den[nt][0] = den[nt][1] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u)
+            o[nt][u][0] = o[nt][u][1] = o[nt][u][2] = o[nt][u][3] = 0.0f;
+    }
+    int kb = k0 + warp * KVP_STEP;
+    load_k(kb);
+    load_v(kb);
+    for (; kb < k1; kb += KVP_WARPS * KVP_STEP) {
+        const bool more = kb + KVP_WARPS * KVP_STEP < k1;
+        float s[2][NT][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(kr[u][0][w], a0, a2);
+                e4m3x4_to_f16(kr[u][1][w], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_16816x(s[u][nt], a0, a1, a2, a3, qb[nt][w][0], qb[nt][w][1]);
+            }
+        }
+        if (more)
+            load_k(kb + KVP_WARPS * KVP_STEP);
+        float xv[2], c[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = (kb + 16 * u - k0) >> 4;
+            const bool in = kb + 16 * u < k1;
+            const float kf = in ? s_kf[i] : 0.0f;
+            xv[u] = in ? s_xv[i] : -INFINITY;
+            c[u] = ex2(-xv[u]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[u][nt][e] = fmaf(s[u][nt][e] * qs[nt][e & 1], kf, xv[u]);
+        }
+        if (kb + KVP_STEP - 1 > rq.len + imin || row0 + R > rows) {  // some row does not see some key
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (kb + 16 * u + g + 8 * (e >> 1) > lim[nt][e & 1])
+                            s[u][nt][e] = -INFINITY;
+        }
+        uint32_t wb[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float corr[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float m = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                m = fmaxf(m, M[nt][e]);
+                const float base = m == -INFINITY ? 0.0f : m;
+                corr[e] = ex2(M[nt][e] - base);
+                M[nt][e] = m;
+                float add = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float w0 = ex2(s[u][nt][e] - base), w1 = ex2(s[u][nt][e + 2] - base);
+                    s[u][nt][e] = w0;
+                    s[u][nt][e + 2] = w1;
+                    add = xv[u] == -INFINITY ? add : fmaf(w0 + w1, c[u], add);
+                }
+                den[nt][e] = fmaf(den[nt][e], corr[e], add);
+            }
+            if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+                for (int u = 0; u < D / 16; ++u) {
+                    o[nt][u][0] *= corr[0];
+                    o[nt][u][1] *= corr[1];
+                    o[nt][u][2] *= corr[0];
+                    o[nt][u][3] *= corr[1];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                wb[u][nt][0] = movmatrix(f16x2_bits(s[u][nt][0], s[u][nt][1]));
+                wb[u][nt][1] = movmatrix(f16x2_bits(s[u][nt][2], s[u][nt][3]));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int w = 0; w < VW; ++w)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t sel = x ? 0x7362u : 0x5140u;
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16(__byte_perm(vr[u][0][w], vr[u][1][w], sel), a0, a1);
+                    e4m3x4_to_f16(__byte_perm(vr[u][2][w], vr[u][3][w], sel), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816x(o[nt][2 * w + x], a0, a1, a2, a3, wb[u][nt][0], wb[u][nt][1]);
+                }
+        if (more)
+            load_v(kb + KVP_WARPS * KVP_STEP);
+    }
+
+    // the warps' shares: lane (g, t) holds dimensions g*D/8 + 2u, +1 of rows 2t, 2t+1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float d = den[nt][e];
+            d += __shfl_xor_sync(0xffffffffu, d, 4);
+            d += __shfl_xor_sync(0xffffffffu, d, 8);
+            d += __shfl_xor_sync(0xffffffffu, d, 16);
+            const int r = 8 * nt + 2 * t + e;
+            if (g == 0) {
+                s_m[warp][r] = M[nt][e];
+                s_den[warp][r] = d;
+            }
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u)
+                *reinterpret_cast<float2 *>(&s_o[warp][r][g * (D / 8) + 2 * u]) = make_float2(o[nt][u][e], o[nt][u][e + 2]);
+        }
+    __syncthreads();
+    const int live_rows = min(R, rows - row0);
+    const int64_t part = ((int64_t)bh * a.tiles + blockIdx.z) * a.S + blockIdx.x;
+    for (int i = tid; i < live_rows * (D / 4); i += KVP_THREADS) {
+        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+        float m = s_m[0][r];
+#pragma unroll
+        for (int w = 1; w < KVP_WARPS; ++w)
+            m = fmaxf(m, s_m[w][r]);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < KVP_WARPS; ++w) {
+            const float f = ex2(s_m[w][r] - base);
+            sum = fmaf(f, s_den[w][r], sum);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = fmaf(f, s_o[w][r][d + j], v[j]);
+        }
+        if (a.S == 1) {
+            const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+            const int rho = row0 + r, tok = rho / a.G, j = rho - tok * a.G;
+            uint2 y;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(v[1] * inv), "f"(v[0] * inv));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(v[3] * inv), "f"(v[2] * inv));
+            *reinterpret_cast<uint2 *>(a.out + ((int64_t)(rq.first + tok) * a.H * a.G + h * a.G + j) * D + d) = y;
+        } else {
+            float *dst = a.ws + (part * R + r) * (D + 4);
+            *reinterpret_cast<float4 *>(dst + d) = make_float4(v[0], v[1], v[2], v[3]);
+            if (d == 0)
+                *reinterpret_cast<float2 *>(dst + D) = make_float2(m, sum);
+        }
+    }
+}
+
+// Joins a row's splits: o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) den_s.  One warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) kv_paged_merge_kernel(KvPagedShape a, int R)
+{
+    const int lane = threadIdx.x & 31;
+    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
+    const int rho = blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_wait();
+    const KvPagedRequest rq = kvp_request(a, b);
+    const int rows = rq.n * a.G;
+    if (rho >= rows)
+        return;
+    const int z = rho / R, r = rho - z * R, i = rho / a.G, j = rho - i * a.G;
+    const int imax = (min((z + 1) * R, rows) - 1) / a.G;
+    const int splits = (rq.len + imax + a.chunk) / a.chunk;  // ceil((len + imax + 1) / chunk)
+    const int64_t step = (int64_t)R * (D + 4);
+    const float *src = a.ws + (((int64_t)bh * a.tiles + z) * a.S * R + r) * (D + 4);
+    float M = -INFINITY;
+    for (int s = lane; s < splits; s += 32)
+        M = fmaxf(M, src[s * step + D]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float base = M == -INFINITY ? 0.0f : M;
+    float den = 0.0f, v[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+        v[k] = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+        const float *p = src + s * step;
+        const float2 md = *reinterpret_cast<const float2 *>(p + D);
+        const float f = ex2(md.x - base);
+        den = fmaf(f, md.y, den);
+        if constexpr (D == 128) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + lane * 4);
+            v[0] = fmaf(f, x.x, v[0]);
+            v[1] = fmaf(f, x.y, v[1]);
+            v[2] = fmaf(f, x.z, v[2]);
+            v[3] = fmaf(f, x.w, v[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(p + lane * 2);
+            v[0] = fmaf(f, x.x, v[0]);
+            v[1] = fmaf(f, x.y, v[1]);
+        }
+    }
+    const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
+    uint32_t y[D / 64];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[k]) : "f"(v[2 * k + 1] * inv), "f"(v[2 * k] * inv));
+    __nv_bfloat16 *dst = a.out + ((int64_t)(rq.first + i) * a.H * a.G + h * a.G + j) * D;
+    if constexpr (D == 128)
+        *reinterpret_cast<uint2 *>(dst + lane * 4) = make_uint2(y[0], y[1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst + lane * 2) = y[0];
+}
+
+}  // namespace fp4lin

@@ -1,0 +1,83 @@
+// mxfp8.cuh -- the 8-bit block format of the serving operators: E4M3 elements under one
+// power-of-two scale per block (a block is 32 values of a row for activations, the rows of one
+// (page, head) for the KV cache), stored as an E8M0 byte.
+//
+// The exponent is the least integer X >= -126 with amax <= 448 * 2^X, so no element saturates
+// (the element with the largest magnitude lands in (224, 448]); byte = X + 127.  E4M3 keeps its
+// relative step over 2^15, so a power of two loses nothing against amax/448 except at the bottom
+// of that range, and re-encoding a block to a larger X is exact down to E4M3's subnormals.
+// Byte 0 is kept for blocks whose maximum is 0: all their codes are zero.
+#pragma once
+
+#include "common.cuh"
+
+namespace fp4lin {
+
+// E8M0 byte of a block whose largest finite magnitude is amax (amax >= 0, finite).
+__device__ __forceinline__ uint32_t mxfp8_scale_byte(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    // floor(log2 amax) - 8, one more when the mantissa passes 448 / 256 = 1.75; subnormal
+    // amax gives -135 or -134 and is raised to -126
+    const int X = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return u == 0u ? 0u : (uint32_t)(max(X, -126) + 127);
+}
+
+// 2^-X for a scale byte (1 for byte 0: that block's values are all zero).
+__device__ __forceinline__ float mxfp8_inverse(uint32_t byte)
+{
+    return byte ? __uint_as_float((254u - byte) << 23) : 1.0f;
+}
+
+// 2^X for a scale byte; byte 0 (all codes zero) gives 2^-127, a binary32 subnormal.
+__device__ __forceinline__ float mxfp8_scale(uint32_t byte)
+{
+    return __uint_as_float(byte ? byte << 23 : 0x400000u);
+}
+
+// |v| where v is finite, else 0: one infinity or NaN does not spoil its block's scale.
+__device__ __forceinline__ float finite_abs(float v)
+{
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// Four floats -> four E4M3 bytes (v[0] in the lowest), round to nearest even, saturating at 448;
+// NaN gives the NaN code.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// Four E4M3 bytes -> two f16x2 (exact): elements 0, 1 and elements 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// Four E4M3 bytes times 2^-k, rounded once to E4M3.  The product is formed in f16: it is exact
+// from 2^-14 up, and everything below 2^-10 (half of E4M3's smallest step) becomes zero anyway.
+__device__ __forceinline__ uint32_t e4m3x4_shift(uint32_t w, uint32_t factor_f16x2)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 p, q;\n\tmov.b32 {l, h}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, l;\n\tcvt.rn.f16x2.e4m3x2 q, h;\n\t"
+        "mul.rn.f16x2 p, p, %2;\n\tmul.rn.f16x2 q, q, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, p;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, q;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "r"(w), "r"(factor_f16x2));
+    return r;
+}
+
+}  // namespace fp4lin

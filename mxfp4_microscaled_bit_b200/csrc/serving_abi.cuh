@@ -1,0 +1,425 @@
+// serving_abi.cuh -- the C ABI of the serving operators (include/fp4lin_serving.h): host-side
+// argument checks and launches.  Part of the library's one translation unit (fp4lin.cu includes it
+// last); it uses that file's host helpers.
+#pragma once
+
+#include "../../include/fp4lin_serving.h"
+#include "kv_paged.cuh"
+#include "kv_paged_attention.cuh"
+#include "matvec.cuh"
+#include "rmsnorm.cuh"
+
+namespace {
+
+// log2 of a page size, or -1 where it is none of 16, 32, 64, 128.
+int page_shift(int page)
+{
+    return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
+}
+
+// Raise a kernel's dynamic shared memory once per device.
+template <typename Kernel>
+int raise_smem(Kernel *kern, bool *done, size_t bytes)
+{
+    std::lock_guard<std::mutex> lk(g_mutex);
+    if (!*done) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+            cudaGetLastError();
+            return FP4LIN_ERR_CUDA;
+        }
+        *done = true;
+    }
+    return FP4LIN_OK;
+}
+
+inline int launched(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return FP4LIN_OK;
+    cudaGetLastError();
+    return FP4LIN_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ norm
+template <int HAD>
+cudaError_t launch_norm(const NormShape &a, cudaStream_t s)
+{
+    const int lanes = (a.cols / 32 + 31) / 32 * 32;
+    if (lanes == 32)
+        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 128>, dim3((unsigned)((a.rows_pad + 3) / 4)), dim3(128), 0, s, a);
+    if (lanes <= 512)
+        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 512>, dim3((unsigned)a.rows_pad), dim3(lanes), 0, s, a);
+    return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 1024>, dim3((unsigned)a.rows_pad), dim3(lanes), 0, s, a);
+}
+
+// ------------------------------------------------------------------ attention
+struct KvPagedPlan {
+    int nt, rows, tiles, chunk, S;
+    size_t ws_bytes;
+};
+
+// Keys a CTA: enough CTAs for several on every SM, in multiples of a step of the CTA's warps.
+KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D, int sms)
+{
+    KvPagedPlan p{};
+    const int64_t most = (int64_t)max_new * G;
+    p.nt = most <= 8 ? 1 : 2;
+    p.rows = 8 * p.nt;
+    p.tiles = (int)((most + p.rows - 1) / p.rows);
+    const int64_t units = (int64_t)B * H * p.tiles;
+    int64_t chunk = (max_len * units + (int64_t)sms * 12 - 1) / ((int64_t)sms * 12);
+    chunk = (chunk + 127) / 128 * 128;
+    chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), KVP_MAX_CHUNK);
+    p.chunk = (int)chunk;
+    p.S = (int)((max_len + chunk - 1) / chunk);
+    p.ws_bytes = p.S > 1 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
+    return p;
+}
+
+bool paged_sizes_ok(int B, int H, int G, int D, int max_new, int64_t max_len)
+{
+    return B >= 1 && H >= 1 && G >= 1 && G <= 16 && (D == 64 || D == 128) && max_new >= 1 && max_len >= 1 &&
+           max_len <= 0x7FFFFFFF - KVP_MAX_CHUNK && (int64_t)B * H <= 65535 && (int64_t)max_new * G <= 65535 * 8;
+}
+
+template <int D>
+cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream_t s)
+{
+    const dim3 grid((unsigned)p.S, (unsigned)(a.B * a.H), (unsigned)p.tiles);
+    cudaError_t e = p.nt == 1 ? launch_pdl(kv_paged_split_kernel<D, 1>, grid, dim3(KVP_THREADS), 0, s, a)
+                              : launch_pdl(kv_paged_split_kernel<D, 2>, grid, dim3(KVP_THREADS), 0, s, a);
+    if (e != cudaSuccess || p.S == 1)
+        return e;
+    const dim3 mgrid((unsigned)(((int64_t)a.max_new * a.G + 3) / 4), (unsigned)(a.B * a.H));
+    return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, p.rows);
+}
+
+// ------------------------------------------------------------------ matvec
+// CTAs a row tile (a cluster's size): the one that keeps the longest CTA shortest, two CTAs an SM;
+// a CTA's start and the cluster's sum cost about two chunks.
+int matvec_ranks(int64_t tiles, int nchunks, int sms)
+{
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int r = 1; r <= 8; ++r) {
+        const int per = (nchunks + r - 1) / r;
+        if ((nchunks + per - 1) / per != r)
+            continue;  // some CTA would have nothing to do
+        const int64_t waves = (tiles * r + 2 * sms - 1) / (2 * sms), cost = waves * (per + 2);
+        if (cost < least) {
+            least = cost;
+            best = r;
+        }
+    }
+    return best;
+}
+
+bool g_matvec_attr[kMaxDevices][16] = {};
+
+template <bool NV, bool X8, int HAD, int NT>
+int launch_matvec(const MatvecShape &a, int tiles, int ranks, int slot, cudaStream_t s)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return FP4LIN_ERR_CUDA;
+    auto *kern = matvec_kernel<NV, X8, HAD, NT>;
+    const int st = raise_smem(kern, &g_matvec_attr[dev][slot], mv_smem(MV_MAX_M, MV_SEG));
+    if (st != FP4LIN_OK)
+        return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * ranks));
+    cfg.blockDim = dim3(MV_THREADS);
+    cfg.dynamicSmemBytes = mv_smem(a.M, std::min(a.per_cta, MV_SEG));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launched(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+template <bool NV, int NT>
+int launch_matvec_x(const MatvecShape &a, int hadamard, int tiles, int ranks, cudaStream_t s)
+{
+    constexpr int base = (NV ? 0 : 6) + (NT - 1) * 3;
+    if (a.xs)
+        return launch_matvec<NV, true, 0, NT>(a, tiles, ranks, base, s);
+    if (hadamard)
+        return launch_matvec<NV, false, NV ? 16 : 32, NT>(a, tiles, ranks, base + 1, s);
+    return launch_matvec<NV, false, 0, NT>(a, tiles, ranks, base + 2, s);
+}
+
+int matvec_entry(bool nv, const void *x, const uint8_t *xs, int64_t M, int64_t K, int64_t ld_x, int hadamard,
+                 const uint8_t *w, const uint8_t *ws, const float *g, void *y, int64_t N, int64_t ldy, void *stream)
+{
+    if (!x || !w || !ws || !y || (nv && !g))
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (M < 1 || N < 1 || K < 1 || ld_x < K || ldy < N)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (hadamard != 0 && (xs || hadamard != (nv ? 16 : 32)))
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (M > MV_MAX_M || K % 64 != 0 || ld_x % (xs ? 16 : 8) != 0 || K > (1 << 24) || N > (1 << 27))
+        return FP4LIN_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(ws, 16) || !aligned(y, 2) || (xs && !aligned(xs, 16)) ||
+        (nv && !aligned(g, 4)))
+        return FP4LIN_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    const int st = current_device(&dev);
+    if (st != FP4LIN_OK)
+        return st;
+    MatvecShape a{};
+    a.x = x;
+    a.xs = xs;
+    a.w = w;
+    a.ws = ws;
+    a.g = g;
+    a.y = reinterpret_cast<__nv_bfloat16 *>(y);
+    a.ld_x = ld_x;
+    a.ldy = ldy;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.katoms_w = (K / (nv ? 16 : 32) + 3) / 4;
+    a.katoms_x = (K / 32 + 3) / 4;
+    a.nchunks = (int)((K + MV_CHUNK - 1) / MV_CHUNK);
+    const int tiles = (int)((N + MV_ROWS - 1) / MV_ROWS);
+    const int ranks = matvec_ranks(tiles, a.nchunks, dev->sms);
+    a.per_cta = (a.nchunks + ranks - 1) / ranks;
+    a.wide_w = aligned(w, 32);
+    cudaStream_t s = as_stream(stream);
+    if (nv)
+        return M <= 8 ? launch_matvec_x<true, 1>(a, hadamard, tiles, ranks, s)
+                      : launch_matvec_x<true, 2>(a, hadamard, tiles, ranks, s);
+    return M <= 8 ? launch_matvec_x<false, 1>(a, hadamard, tiles, ranks, s)
+                  : launch_matvec_x<false, 2>(a, hadamard, tiles, ranks, s);
+}
+
+bool g_table_attr[kMaxDevices] = {};
+
+}  // namespace
+
+extern "C" {
+
+int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_r, const void *weight, float eps,
+                  int hadamard, int64_t rows, int64_t cols, uint8_t *codes, uint8_t *scales, void *summed,
+                  int64_t ld_s, void *stream)
+{
+    if (!x || !weight || !codes || !scales || (residual == nullptr) != (summed == nullptr))
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (rows < 1 || cols < 1 || ld_x < cols || (residual && (ld_r < cols || ld_s < cols)) || !(eps >= 0.0f) ||
+        eps > 3.4e38f)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (hadamard != 0 && hadamard != 16 && hadamard != 32)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (cols % 32 != 0 || cols > NORM_MAX_COLS || rows > (1 << 30) || ld_x % 8 != 0 ||
+        (residual && (ld_r % 8 != 0 || ld_s % 8 != 0)))
+        return FP4LIN_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(codes, 16) || !aligned(scales, 16) ||
+        (residual && (!aligned(residual, 16) || !aligned(summed, 16))))
+        return FP4LIN_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    const int st = current_device(&dev);
+    if (st != FP4LIN_OK)
+        return st;
+    NormShape a{};
+    a.x = reinterpret_cast<const __nv_bfloat16 *>(x);
+    a.r = reinterpret_cast<const __nv_bfloat16 *>(residual);
+    a.w = reinterpret_cast<const __nv_bfloat16 *>(weight);
+    a.s = reinterpret_cast<__nv_bfloat16 *>(summed);
+    a.codes = codes;
+    a.scales = scales;
+    a.rows = rows;
+    a.rows_pad = (rows + 127) / 128 * 128;
+    a.cols = (int)cols;
+    a.ld_x = ld_x;
+    a.ld_r = ld_r;
+    a.ld_s = ld_s;
+    a.katoms = (cols / 32 + 3) / 4;
+    a.eps = eps;
+    a.inv_cols = 1.0f / (float)cols;
+    a.wide_x = aligned(x, 32) && ld_x % 16 == 0;
+    a.wide_r = residual && aligned(residual, 32) && ld_r % 16 == 0;
+    a.wide_s = residual && aligned(summed, 32) && ld_s % 16 == 0;
+    a.wide_w = aligned(weight, 32);
+    a.wide_c = aligned(codes, 32);
+    cudaStream_t s = as_stream(stream);
+    return launched(hadamard == 16   ? launch_norm<16>(a, s)
+                    : hadamard == 32 ? launch_norm<32>(a, s)
+                                     : launch_norm<0>(a, s));
+}
+
+int nvfp4_matvec(const void *x, const uint8_t *x_scales, int64_t M, int64_t K, int64_t ld_x, int hadamard,
+                 const uint8_t *w_codes, const uint8_t *w_scales, const float *g_w, void *y, int64_t N, int64_t ldy,
+                 void *stream)
+{
+    return matvec_entry(true, x, x_scales, M, K, ld_x, hadamard, w_codes, w_scales, g_w, y, N, ldy, stream);
+}
+
+int mxfp4_matvec(const void *x, const uint8_t *x_scales, int64_t M, int64_t K, int64_t ld_x, int hadamard,
+                 const uint8_t *w_codes, const uint8_t *w_scales, void *y, int64_t N, int64_t ldy, void *stream)
+{
+    return matvec_entry(false, x, x_scales, M, K, ld_x, hadamard, w_codes, w_scales, nullptr, y, N, ldy, stream);
+}
+
+int kv_block_tables(int32_t *table, int64_t ld_table, int width, const int32_t *lens, const int32_t *new_lens, int B,
+                    const int32_t *free_pages, int num_free, const int32_t *free_head, int page, int max_tokens,
+                    int32_t *cu_new, int32_t *slots, int32_t *next_head, void *stream)
+{
+    if (!table || !lens || !new_lens || !free_pages || !free_head || !cu_new || !slots || !next_head)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (B < 1 || width < 1 || ld_table < width || num_free < 1 || max_tokens < 1 || free_head == next_head)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    const int shift = page_shift(page);
+    if (shift < 0 || B > TABLE_MAX_REQUESTS || max_tokens > (1 << 30) || ((int64_t)width << shift) > 0x7FFFFFFF)
+        return FP4LIN_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_head, 4) || !aligned(cu_new, 4) || !aligned(slots, 4) || !aligned(next_head, 4))
+        return FP4LIN_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    int st = current_device(&dev);
+    if (st != FP4LIN_OK)
+        return st;
+    int ordinal = 0;
+    if (cudaGetDevice(&ordinal) != cudaSuccess)
+        return FP4LIN_ERR_CUDA;
+    st = raise_smem(kv_table_kernel, &g_table_attr[ordinal], table_smem(TABLE_MAX_REQUESTS));
+    if (st != FP4LIN_OK)
+        return st;
+    TableShape a{};
+    a.table = table;
+    a.lens = lens;
+    a.new_lens = new_lens;
+    a.free_list = free_pages;
+    a.head = free_head;
+    a.cu = cu_new;
+    a.slots = slots;
+    a.next_head = next_head;
+    a.ld = ld_table;
+    a.B = B;
+    a.width = width;
+    a.F = num_free;
+    a.max_tokens = max_tokens;
+    a.shift = shift;
+    const int64_t items = std::max<int64_t>(max_tokens, (int64_t)(max_tokens >> shift) + B + 1);
+    const int64_t grid = std::min<int64_t>((items + TABLE_THREADS - 1) / TABLE_THREADS, dev->sms);
+    return launched(launch_pdl(kv_table_kernel, dim3((unsigned)grid), dim3(TABLE_THREADS), table_smem(B),
+                               as_stream(stream), a));
+}
+
+int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_v, const int32_t *slots, int T,
+                 uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales, int num_pages, int H,
+                 int page, int D, void *stream)
+{
+    if (!k_new || !v_new || !slots || !k_codes || !k_scales || !v_codes || !v_scales)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (T < 1 || H < 1 || D < 1 || num_pages < 1 || ld_k < (int64_t)H * D || ld_v < (int64_t)H * D)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    const int shift = page_shift(page);
+    if (shift < 0 || (D != 64 && D != 128) || ld_k % 8 != 0 || ld_v % 8 != 0 || H > 32767 ||
+        ((int64_t)num_pages << shift) > 0x7FFFFFFF)
+        return FP4LIN_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
+        !aligned(slots, 4))
+        return FP4LIN_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    const int st = current_device(&dev);
+    if (st != FP4LIN_OK)
+        return st;
+    AppendShape a{};
+    a.k = reinterpret_cast<const __nv_bfloat16 *>(k_new);
+    a.v = reinterpret_cast<const __nv_bfloat16 *>(v_new);
+    a.slots = slots;
+    a.kc = k_codes;
+    a.ks = k_scales;
+    a.vc = v_codes;
+    a.vs = v_scales;
+    a.ld_k = ld_k;
+    a.ld_v = ld_v;
+    a.slots_end = (int64_t)num_pages << shift;
+    a.T = T;
+    a.H = H;
+    a.shift = shift;
+    // fewer tokens a CTA while there are fewer CTAs than the SMs hold
+    a.per_cta = APPEND_TOKENS;
+    while (a.per_cta > 1 && (int64_t)((T + a.per_cta - 1) / a.per_cta) * H * 2 < (int64_t)dev->sms * 8)
+        a.per_cta /= 2;
+    const dim3 grid((unsigned)((T + a.per_cta - 1) / a.per_cta), (unsigned)(2 * H));
+    cudaStream_t s = as_stream(stream);
+    return launched(D == 64 ? launch_pdl(kv_append_kernel<64>, grid, dim3(APPEND_THREADS), 0, s, a)
+                            : launch_pdl(kv_append_kernel<128>, grid, dim3(APPEND_THREADS), 0, s, a));
+}
+
+size_t kv_fp8_attention_workspace_bytes(int B, int H, int G, int max_new, int64_t max_len, int D)
+{
+    if (!paged_sizes_ok(B, H, G, D, max_new, max_len))
+        return 0;
+    int sms = 148, dev = 0, v = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && v > 0)
+        sms = v;
+    else
+        cudaGetLastError();
+    return plan_paged(B, H, G, max_new, max_len, D, sms).ws_bytes;
+}
+
+int kv_fp8_attention(const void *q, int64_t ld_q, int T, const uint8_t *k_codes, const uint8_t *k_scales,
+                     const uint8_t *v_codes, const uint8_t *v_scales, int num_pages, int page, const int32_t *table,
+                     int64_t ld_table, int width, const int32_t *lens, const int32_t *cu_new, int max_new,
+                     int64_t max_len, float scale, void *out, int B, int H, int G, int D, void *workspace,
+                     size_t workspace_bytes, void *stream)
+{
+    if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !table || !lens || !cu_new || !out)
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    if (B < 1 || H < 1 || G < 1 || D < 1 || T < 1 || num_pages < 1 || width < 1 || ld_table < width || max_new < 1 ||
+        max_len < 1 || ld_q < (int64_t)H * G * D || !(scale >= -3.4e38f && scale <= 3.4e38f))
+        return FP4LIN_ERR_INVALID_ARGUMENT;
+    const int shift = page_shift(page);
+    if (shift < 0 || !paged_sizes_ok(B, H, G, D, max_new, max_len) || ld_q % 8 != 0 ||
+        ((int64_t)num_pages << shift) > 0x7FFFFFFF)
+        return FP4LIN_ERR_UNSUPPORTED_SHAPE;
+    if (max_len > ((int64_t)width << shift))
+        return FP4LIN_ERR_INVALID_ARGUMENT;  // the table cannot hold max_len rows
+    if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(out, 16) || !aligned(table, 4) ||
+        !aligned(lens, 4) || !aligned(cu_new, 4) || (workspace && !aligned(workspace, 16)))
+        return FP4LIN_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    const int st = current_device(&dev);
+    if (st != FP4LIN_OK)
+        return st;
+    const KvPagedPlan p = plan_paged(B, H, G, max_new, max_len, D, dev->sms);
+    if (p.ws_bytes && (!workspace || workspace_bytes < p.ws_bytes))
+        return FP4LIN_ERR_WORKSPACE;
+    KvPagedShape a{};
+    a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    a.kc = k_codes;
+    a.ks = k_scales;
+    a.vc = v_codes;
+    a.vs = v_scales;
+    a.table = table;
+    a.lens = lens;
+    a.cu = cu_new;
+    a.out = reinterpret_cast<__nv_bfloat16 *>(out);
+    a.ws = reinterpret_cast<float *>(workspace);
+    a.ld_q = ld_q;
+    a.ld_t = ld_table;
+    a.qscale = scale * 1.4426950408889634f;
+    a.B = B;
+    a.H = H;
+    a.G = G;
+    a.T = T;
+    a.NP = num_pages;
+    a.shift = shift;
+    a.max_new = max_new;
+    a.max_len = (int)max_len;
+    a.chunk = p.chunk;
+    a.S = p.S;
+    a.tiles = p.tiles;
+    cudaStream_t s = as_stream(stream);
+    return launched(D == 64 ? launch_paged<64>(a, p, s) : launch_paged<128>(a, p, s));
+}
+
+}  // extern "C"
