@@ -37,6 +37,7 @@ struct KvPagedShape {
     float qscale;            // scale * log2(e)
     int B, H, G, T, NP, shift, max_new, max_len;
     int chunk, S, tiles;
+    int max_rows;            // requests of more rows are the tensor-core kernel's (kv_paged_prefill.cuh)
 };
 
 // One request as a CTA sees it; ok is false where the lengths cannot be what the caller promised
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
     if (!rq.ok && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0)
         report_error(FP4LIN_ERR_OUT_OF_RANGE);
     const int rows = rq.n * a.G, row0 = blockIdx.z * R;
-    if (row0 >= rows)
+    if (row0 >= rows || rows > a.max_rows)
         return;
     const int imin = row0 / a.G, imax = (min(row0 + R, rows) - 1) / a.G;
     const int k0 = blockIdx.x * a.chunk, kend = rq.len + imax + 1;  // keys the tile's last row sees
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(128) kv_paged_merge_kernel(KvPagedShape a, int
     pdl_wait();
     const KvPagedRequest rq = kvp_request(a, b);
     const int rows = rq.n * a.G;
-    if (rho >= rows)
+    if (rho >= rows || rows > a.max_rows)
         return;
     const int z = rho / R, r = rho - z * R, i = rho / a.G, j = rho - i * a.G;
     const int imax = (min((z + 1) * R, rows) - 1) / a.G;

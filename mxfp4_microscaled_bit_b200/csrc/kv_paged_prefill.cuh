@@ -1,0 +1,503 @@
+// kv_paged_prefill.cuh -- kv_paged_attention.cuh's attention for requests with many new tokens: the
+// same mathematics on tcgen05.
+//
+// Bound by the tensor cores and, as closely, by the exponentials (4 D flops and one exponential a
+// score: at D = 128 a 256 x 128 block of scores takes ~2050 cycles of either).  One CTA an SM takes
+// 256 (token, head) rows of one kv head, as two tiles of 128: while the softmax of one runs, the
+// tensor cores work on the other, and every key block that is converted serves both.
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread owns a row.  Reads the row's 128 scores from TMEM,
+//                    applies both scales in one multiply-add, writes the f16 weights over the scores
+//                    in TMEM.  The output is rescaled only when the maximum has grown by more than
+//                    2^8 (the weights stay below 2^8, far inside f16), which is rare.
+//   warps 8-11       load 128 keys of K and V from their pages, a block ahead in registers, and
+//                    write them as f16 (exact) in the 128-byte-swizzled operand layout.
+//   warp 12          issues the MMAs: S = Q K^T (both in shared memory, K-major) and O += P V (P from
+//                    TMEM, V as an MN-major operand: its rows are keys, as in the cache).
+// TMEM: scores and weights of the tiles in columns 0 and 128, outputs in 256 and 256 + D.
+#pragma once
+
+#include "kv_paged_attention.cuh"
+
+namespace fp4lin {
+
+constexpr int KPP_THREADS = 512;
+constexpr int KPP_KEYS = 128;          // keys a block
+constexpr int KPP_ROWS = 256;          // rows a CTA
+constexpr int KPP_SLOTS = 4;           // blocks whose page factors are held at once
+constexpr float KPP_LAZY = 8.0f;       // log2 growth of the maximum that is let pass
+
+struct KppCtrl {
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], odone[2], drain;
+    float kf[KPP_SLOTS][8], xv[KPP_SLOTS][8], c[KPP_SLOTS][8];
+    uint32_t tmem;
+    int abort, nan;
+};
+
+constexpr size_t kpp_smem(int D) { return 1024 + (size_t)(KPP_ROWS + 4 * KPP_KEYS) * D * 2 + sizeof(KppCtrl); }
+
+// D[128 x N] (+)= A[128 x 16] B[N x 16]^T, f16 operands: A in shared memory, or (ts) in TMEM.
+__device__ __forceinline__ void mma_f16_ss_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+
+// MN-major operand, 128-byte swizzle: rows (k) of 128 bytes = 64 values along MN, 8-row groups 1024
+// bytes apart (stride byte offset), the next 64 values `lbo` bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16: binary32 accumulator, f16 operands, M = 128.
+constexpr uint32_t kpp_idesc(int N, bool b_mn_major)
+{
+    return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(N / 8) << 17) | ((128u / 16u) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                   "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Waits for this thread's tcgen05.ld; the registers go through it so that none is read before.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+                 : "memory");
+}
+
+// 8 columns, loaded, scaled by f and stored back.
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Bytes of w that are the E4M3 NaN code become 0; true if there was one.
+__device__ __forceinline__ bool drop_nan_codes(uint32_t &w)
+{
+    const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w &= ~m;
+    return m != 0u;
+}
+
+// 16 codes of (row, 16-byte chunk cc of the row) as f16 into the operand layout at `base`: blocks of
+// 128 rows x 128 bytes, one for each 64 dimensions; 16-byte chunk x of row r sits at x ^ (r % 8).
+template <int D>
+__device__ __forceinline__ void kpp_convert(uint8_t *base, int row, int cc, uint4 u)
+{
+    uint32_t f[8];
+    e4m3x4_to_f16(u.x, f[0], f[1]);
+    e4m3x4_to_f16(u.y, f[2], f[3]);
+    e4m3x4_to_f16(u.z, f[4], f[5]);
+    e4m3x4_to_f16(u.w, f[6], f[7]);
+    uint8_t *p = base + (cc >> 2) * (KPP_KEYS * 128) + row * 128;
+    const int c0 = 2 * (cc & 3), sw = row & 7;
+    // lanes of the upper dimensions store their odd chunk first: a quarter warp then meets each bank once
+    const bool odd = cc >> 2;
+    *reinterpret_cast<uint4 *>(p + (((c0 + odd) ^ sw) << 4)) =
+        odd ? make_uint4(f[4], f[5], f[6], f[7]) : make_uint4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<uint4 *>(p + (((c0 + !odd) ^ sw) << 4)) =
+        odd ? make_uint4(f[0], f[1], f[2], f[3]) : make_uint4(f[4], f[5], f[6], f[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a, int min_rows)
+{
+    extern __shared__ uint8_t kpp_raw[];
+    uint8_t *sm = kpp_raw + ((1024u - (smem_u32(kpp_raw) & 1023u)) & 1023u);
+    constexpr int TILE = 128 * D * 2;  // bytes of an operand tile
+    uint8_t *s_q = sm, *s_k = sm + 2 * TILE, *s_v = sm + 4 * TILE;
+    KppCtrl &ct = *reinterpret_cast<KppCtrl *>(sm + 6 * TILE);
+    volatile int *abort = &ct.abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
+    pdl_wait();
+    const KvPagedRequest rq = kvp_request(a, b);
+    const int rows = rq.n * a.G;
+    const int row0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * KPP_ROWS;  // longest first
+    if (rows < min_rows || row0 >= rows)
+        return;
+    const int live = min(KPP_ROWS, rows - row0);
+    const int tiles = live > 128 ? 2 : 1;
+    const int imin = row0 / a.G, imax = (row0 + live - 1) / a.G;
+    const int kend = rq.len + imax + 1;            // keys that the last row sees
+    const int blocks = (kend + KPP_KEYS - 1) / KPP_KEYS;
+    const int all = rq.len + imin;                 // last key that every row sees
+    const int P1 = (1 << a.shift) - 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.kfull[i], 128);
+            mbar_init(&ct.kfree[i], 1);
+            mbar_init(&ct.vfull[i], 128);
+            mbar_init(&ct.vfree[i], 1);
+            mbar_init(&ct.sfull[i], 2);
+            mbar_init(&ct.pfull[i], 128);
+            mbar_init(&ct.odone[i], 2);
+        }
+        mbar_init(&ct.drain, 1);
+        ct.abort = 0;
+        ct.nan = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ct.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // q: a thread's own row, to f16 at [1, 2) times its code, into the operand layout
+    float qs = 0.0f;
+    const int tile = warp >> 2, trow = tid & 127;
+    const int rho = row0 + tid, tok = rho / a.G, head = rho - tok * a.G;
+    const bool mine = tid < live;
+    if (warp < 8) {
+        const __nv_bfloat16 *src =
+            a.q + (int64_t)(rq.first + (mine ? tok : 0)) * a.ld_q + (int64_t)(h * a.G + (mine ? head : 0)) * D;
+        float m = 0.0f;
+        for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            bf16x8_to_f32(mine ? ld_nc_v4(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                m = fmaxf(m, finite_abs(f[j]));
+        }
+        const uint32_t e = m > 0.0f ? min(max(__float_as_uint(m) >> 23, 1u), 253u) : 127u;
+        const float inv = __uint_as_float((254u - e) << 23);
+        qs = __uint_as_float(e << 23) * a.qscale;
+        for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            bf16x8_to_f32(mine ? ld_nc_v4(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), f);
+            uint4 v;
+            v.x = cvt_f16x2(f[0] * inv, f[1] * inv);
+            v.y = cvt_f16x2(f[2] * inv, f[3] * inv);
+            v.z = cvt_f16x2(f[4] * inv, f[5] * inv);
+            v.w = cvt_f16x2(f[6] * inv, f[7] * inv);
+            *reinterpret_cast<uint4 *>(s_q + tile * TILE + (i >> 3) * (128 * 128) + trow * 128 +
+                                       (((i & 7) ^ (trow & 7)) << 4)) = v;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ct.tmem;
+
+    if (warp < 8) {
+        if (tile < tiles) {
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
+            const uint32_t t_s = tmem + lanes + tile * 128, t_o = tmem + lanes + 256 + tile * D;
+            const int lim = mine ? rq.len + tok : -1;
+            float M = -INFINITY, den = 0.0f;
+            bool ok = true;
+            for (int i = 0; i < blocks; ++i) {
+                ok = warp_wait(&ct.sfull[tile], i & 1, abort, lane);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int slot = i & (KPP_SLOTS - 1), k0 = i * KPP_KEYS;
+                const bool masked = k0 + KPP_KEYS - 1 > all || live < KPP_ROWS;
+                uint32_t s[2][32];  // two chunks of the row: one is worked on while the next arrives
+                // s' = log2(e) s + Xv, -inf where the row does not see the key
+                auto scale_chunk = [&](int k, uint32_t *v) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const float f = ct.kf[slot][2 * k + g] * qs, x = ct.xv[slot][2 * k + g];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[16 * g + j] = __float_as_uint(fmaf(__uint_as_float(v[16 * g + j]), f, x));
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (k0 + 32 * k + j > lim)
+                                v[j] = 0xFF800000u;
+                    }
+                };
+                // the row is read twice, for its maximum and for its weights: held once, its 128 scores
+                // and their packing need more registers than sixteen warps have
+                float m = -INFINITY;
+                tmem_ld32_issue(t_s, s[0]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    tmem_ld_wait(s[k & 1]);
+                    if (k < 3)
+                        tmem_ld32_issue(t_s + 32 * (k + 1), s[(k + 1) & 1]);
+                    scale_chunk(k, s[k & 1]);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        m = max3f(m, __uint_as_float(s[k & 1][j]), __uint_as_float(s[k & 1][j + 1]));
+                }
+                tmem_ld32_issue(t_s, s[0]);
+                float corr = 1.0f;
+                if (m > M + KPP_LAZY || (M == -INFINITY && m > M)) {
+                    corr = ex2(M - m);  // 0 for the first keys
+                    M = m;
+                }
+                if (__any_sync(0xffffffffu, corr != 1.0f) && i > 0) {
+                    ok = warp_wait(&ct.odone[tile], (i - 1) & 1, abort, lane);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll 2
+                    for (int k = 0; k < D / 8; ++k)
+                        tmem_scale8(t_o + 8 * k, corr);
+                }
+                den *= corr;
+                const float base = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    tmem_ld_wait(s[k & 1]);
+                    if (k < 3)
+                        tmem_ld32_issue(t_s + 32 * (k + 1), s[(k + 1) & 1]);
+                    scale_chunk(k, s[k & 1]);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float w0 = ex2(__uint_as_float(s[k & 1][16 * g + j]) - base);
+                            const float w1 = ex2(__uint_as_float(s[k & 1][16 * g + j + 1]) - base);
+                            sum += w0 + w1;
+                            w[8 * g + j / 2] = cvt_f16x2(w0, w1);
+                        }
+                        den = fmaf(sum, ct.c[slot][2 * k + g], den);
+                    }
+                    tmem_st16(t_s + 16 * k, w);  // columns that have been read already
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&ct.pfull[tile]);
+            }
+            if (ok && warp_wait(&ct.odone[tile], (blocks - 1) & 1, abort, lane)) {
+                tc_fence_after();
+                const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
+                __nv_bfloat16 *dst =
+                    a.out + (int64_t)(rq.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_ld32_issue(t_o + 32 * k, o);
+                    tmem_ld_wait(o);
+                    if (mine)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                                    : "=r"(y[e])
+                                    : "f"(__uint_as_float(o[j + 2 * e + 1]) * inv), "f"(__uint_as_float(o[j + 2 * e]) * inv));
+                            st_v4(dst + 32 * k + j, make_uint4(y[0], y[1], y[2], y[3]));
+                        }
+                }
+                if (ct.nan && mine) {  // a NaN value code among the keys that not every row sees
+                    for (int key = all + 1; key <= lim; ++key) {
+                        const int page = a.table[b * a.ld_t + (key >> a.shift)];
+                        if (page < 0 || page >= a.NP)
+                            continue;
+                        const uint8_t *v = a.vc + ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D;
+                        for (int d = 0; d < D; ++d)
+                            if ((v[d] & 127) == 127)
+                                dst[d] = __ushort_as_bfloat16(0x7FC0);
+                    }
+                }
+            }
+        }
+    } else if (warp < 12) {
+        constexpr int CPR = D / 16, RPP = 128 / CPR, PASSES = KPP_KEYS / RPP;  // 16-byte chunks a row, rows a pass
+        const int u = tid - 256, cc = u % CPR, r0 = u / CPR;
+        const int32_t *table = a.table + b * a.ld_t;
+        // lane g < 8 holds the page of the block's keys 16 g ..
+        auto pages_of = [&](int i) {
+            const int key = i * KPP_KEYS + 16 * (lane & 7);
+            int page = -1;
+            if (key < kend) {
+                page = table[key >> a.shift];
+                if (page < 0 || page >= a.NP) {
+                    page = -1;
+                    report_error(FP4LIN_ERR_OUT_OF_RANGE);
+                }
+            }
+            return page;
+        };
+        auto load = [&](const uint8_t *codes, int i, int pages, uint4 *x) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int row = r0 + p * RPP, key = i * KPP_KEYS + row;
+                const int page = __shfl_sync(0xffffffffu, pages, row >> 4);
+                x[p] = page >= 0 && key < kend
+                           ? ld_nc_v4(codes + ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D + 16 * cc)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        uint4 xk[PASSES], xv[PASSES];
+        int pages = pages_of(0);
+        load(a.kc, 0, pages, xk);
+        load(a.vc, 0, pages, xv);
+        for (int i = 0; i < blocks; ++i) {
+            const int next = i + 1 < blocks ? pages_of(i + 1) : -1;
+            const int st = i & 1, par = ((i >> 1) & 1) ^ 1;
+            if (i >= 2 && !warp_wait(&ct.kfree[st], par, abort, lane))
+                break;
+            if (warp == 8 && lane < 8) {
+                const int slot = i & (KPP_SLOTS - 1);
+                const uint32_t kb = pages >= 0 ? a.ks[(int64_t)pages * a.H + h] : 0u;
+                const uint32_t vb = pages >= 0 ? a.vs[(int64_t)pages * a.H + h] : 0u;
+                const float x = vb ? (float)((int)vb - 127) : KVP_ZERO_X;
+                ct.kf[slot][lane] = mxfp8_scale(kb);
+                ct.xv[slot][lane] = pages >= 0 ? x : -INFINITY;
+                ct.c[slot][lane] = pages >= 0 ? ex2(-x) : 0.0f;
+            }
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+                kpp_convert<D>(s_k + st * TILE, r0 + p * RPP, cc, xk[p]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&ct.kfull[st]);
+            if (i + 1 < blocks)
+                load(a.kc, i + 1, next, xk);
+            if (i >= 2 && !warp_wait(&ct.vfree[st], par, abort, lane))
+                break;
+            if ((i + 1) * KPP_KEYS - 1 > all) {  // keys that some rows do not see: weight 0 must stay 0
+                bool nan = false;
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p)
+                    if (i * KPP_KEYS + r0 + p * RPP > all)
+                        nan |= drop_nan_codes(xv[p].x) | drop_nan_codes(xv[p].y) | drop_nan_codes(xv[p].z) |
+                               drop_nan_codes(xv[p].w);
+                if (nan)
+                    ct.nan = 1;
+            }
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+                kpp_convert<D>(s_v + st * TILE, r0 + p * RPP, cc, xv[p]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&ct.vfull[st]);
+            if (i + 1 < blocks)
+                load(a.vc, i + 1, next, xv);
+            pages = next;
+        }
+    } else {
+        if (warp == 12) {
+            constexpr uint32_t IQK = kpp_idesc(KPP_KEYS, false), IPV = kpp_idesc(D, true);
+            auto scores = [&](int j, int i) {
+                const uint32_t qa = smem_u32(s_q + j * TILE), ka = smem_u32(s_k + (i & 1) * TILE);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+                    mma_f16_ss_w(tmem + j * 128, desc_sw128(qa + off), desc_sw128(ka + off), IQK, k > 0);
+                }
+                tc_commit_w(&ct.sfull[j]);
+                if (lane == 0)
+                    mbar_arrive(&ct.sfull[j]);  // passes on what kfull released (the page factors)
+            };
+            auto values = [&](int j, int i) {
+                const uint32_t va = smem_u32(s_v + (i & 1) * TILE);
+#pragma unroll
+                for (int k = 0; k < KPP_KEYS / 16; ++k)
+                    mma_f16_ts_w(tmem + 256 + j * D, tmem + j * 128 + 8 * k, desc_sw128_mn(va + k * 2048, KPP_KEYS * 128),
+                                 IPV, i > 0 || k > 0);
+                tc_commit_w(&ct.odone[j]);
+                if (lane == 0)
+                    mbar_arrive(&ct.odone[j]);  // and on what vfull released
+            };
+            bool ok = warp_poll(&ct.kfull[0], 0, abort, lane);
+            if (ok) {
+                tc_fence_after();
+                for (int j = 0; j < tiles; ++j)
+                    scores(j, 0);
+                tc_commit_w(&ct.kfree[0]);
+            }
+            for (int i = 0; ok && i < blocks; ++i) {
+                const int st = i & 1, par = (i >> 1) & 1;
+                ok = warp_poll(&ct.vfull[st], par, abort, lane);
+                if (ok && i + 1 < blocks)
+                    ok = warp_poll(&ct.kfull[st ^ 1], ((i + 1) >> 1) & 1, abort, lane);
+                for (int j = 0; ok && j < tiles; ++j) {
+                    ok = warp_poll(&ct.pfull[j], i & 1, abort, lane);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    values(j, i);
+                    if (i + 1 < blocks)
+                        scores(j, i + 1);
+                }
+                if (ok) {
+                    tc_commit_w(&ct.vfree[st]);
+                    if (i + 1 < blocks)
+                        tc_commit_w(&ct.kfree[st ^ 1]);
+                }
+            }
+            // nothing may be in flight when TMEM goes and the shared memory with it
+            tc_commit_w(&ct.drain);
+            if (lane == 0)
+                wait_bounded(&ct.drain, 0, abort, false);
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+}  // namespace fp4lin

@@ -6,6 +6,7 @@
 #include "../../include/fp4lin_serving.h"
 #include "kv_paged.cuh"
 #include "kv_paged_attention.cuh"
+#include "kv_paged_prefill.cuh"
 #include "matvec.cuh"
 #include "rmsnorm.cuh"
 
@@ -53,8 +54,13 @@ cudaError_t launch_norm(const NormShape &a, cudaStream_t s)
 }
 
 // ------------------------------------------------------------------ attention
+// Requests of at most KVP_SPLIT_ROWS (token, head) rows are the split kernel's, which streams the
+// cache at HBM speed; the others the tensor-core kernel's.
+constexpr int KVP_SPLIT_ROWS = 16;
+
 struct KvPagedPlan {
-    int nt, rows, tiles, chunk, S;
+    int nt, rows, tiles, chunk, S, max_rows;
+    int prefill_tiles;  // 0: no request can have more than KVP_SPLIT_ROWS rows
     size_t ws_bytes;
 };
 
@@ -62,7 +68,9 @@ struct KvPagedPlan {
 KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D, int sms)
 {
     KvPagedPlan p{};
-    const int64_t most = (int64_t)max_new * G;
+    const int64_t all = (int64_t)max_new * G, most = std::min<int64_t>(all, KVP_SPLIT_ROWS);
+    p.max_rows = KVP_SPLIT_ROWS;
+    p.prefill_tiles = all > KVP_SPLIT_ROWS ? (int)((all + KPP_ROWS - 1) / KPP_ROWS) : 0;
     p.nt = most <= 8 ? 1 : 2;
     p.rows = 8 * p.nt;
     p.tiles = (int)((most + p.rows - 1) / p.rows);
@@ -76,6 +84,8 @@ KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D,
     return p;
 }
 
+bool g_prefill_attr[kMaxDevices][2] = {};
+
 bool paged_sizes_ok(int B, int H, int G, int D, int max_new, int64_t max_len)
 {
     return B >= 1 && H >= 1 && G >= 1 && G <= 16 && (D == 64 || D == 128) && max_new >= 1 && max_len >= 1 &&
@@ -85,12 +95,18 @@ bool paged_sizes_ok(int B, int H, int G, int D, int max_new, int64_t max_len)
 template <int D>
 cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream_t s)
 {
+    if (p.prefill_tiles) {
+        const cudaError_t e = launch_pdl(kv_paged_prefill_kernel<D>, dim3((unsigned)p.prefill_tiles, (unsigned)(a.B * a.H)),
+                                         dim3(KPP_THREADS), kpp_smem(D), s, a, p.max_rows + 1);
+        if (e != cudaSuccess)
+            return e;
+    }
     const dim3 grid((unsigned)p.S, (unsigned)(a.B * a.H), (unsigned)p.tiles);
     cudaError_t e = p.nt == 1 ? launch_pdl(kv_paged_split_kernel<D, 1>, grid, dim3(KVP_THREADS), 0, s, a)
                               : launch_pdl(kv_paged_split_kernel<D, 2>, grid, dim3(KVP_THREADS), 0, s, a);
     if (e != cudaSuccess || p.S == 1)
         return e;
-    const dim3 mgrid((unsigned)(((int64_t)a.max_new * a.G + 3) / 4), (unsigned)(a.B * a.H));
+    const dim3 mgrid((unsigned)((std::min<int64_t>((int64_t)a.max_new * a.G, p.max_rows) + 3) / 4), (unsigned)(a.B * a.H));
     return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, p.rows);
 }
 
@@ -418,6 +434,16 @@ int kv_fp8_attention(const void *q, int64_t ld_q, int T, const uint8_t *k_codes,
     a.chunk = p.chunk;
     a.S = p.S;
     a.tiles = p.tiles;
+    a.max_rows = p.max_rows;
+    if (p.prefill_tiles) {
+        int ordinal = 0;
+        if (cudaGetDevice(&ordinal) != cudaSuccess)
+            return FP4LIN_ERR_CUDA;
+        const int ready = D == 64 ? raise_smem(kv_paged_prefill_kernel<64>, &g_prefill_attr[ordinal][0], kpp_smem(64))
+                                  : raise_smem(kv_paged_prefill_kernel<128>, &g_prefill_attr[ordinal][1], kpp_smem(128));
+        if (ready != FP4LIN_OK)
+            return ready;
+    }
     cudaStream_t s = as_stream(stream);
     return launched(D == 64 ? launch_paged<64>(a, p, s) : launch_paged<128>(a, p, s));
 }

@@ -30,9 +30,15 @@ SERVING_EXPORTS = {
 _BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 
 
+_library = None
+
+
 def _lib():
-    from . import lib
-    return lib()
+    global _library
+    if _library is None:
+        from . import lib
+        _library = lib()
+    return _library
 
 
 def _fail(fn: str, status: int):
@@ -40,70 +46,73 @@ def _fail(fn: str, status: int):
     raise Fp4LinError(fn, status)
 
 
-def _arg(fn: str, name: str, t, dtype, count: int, dev: int) -> int:
-    """t: a contiguous `dtype` tensor of at least `count` values on device `dev`; its address."""
+def _refuse(fn: str, name: str, t, dtype, dev: int) -> None:
+    """Raise for what _arg and _rows have in common, if that is what is wrong with t."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor, not {type(t).__name__}")
     if t.dtype is not dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
-    _place(fn, name, t, dev)
-    if t.numel() < count:
-        raise ValueError(f"{fn}: {name} holds {t.numel()} values, the call needs {count}")
-    return t.data_ptr()
-
-
-def _place(fn: str, name: str, t: torch.Tensor, dev: int) -> None:
     if not t.is_cuda:
         raise ValueError(f"{fn}: {name} must be a CUDA tensor, not on {t.device}")
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}; the library works on the current device cuda:{dev}")
 
 
-def _rows(fn: str, name: str, t, dtype, shape, dev: int) -> int:
-    """t: a `dtype` tensor of this shape whose rows (all dimensions but the first) are contiguous;
-    its first dimension's stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{fn}: {name} must be a torch.Tensor, not {type(t).__name__}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _arg(fn: str, name: str, t, dtype, count: int, dev: int) -> int:
+    """t: a contiguous `dtype` tensor of at least `count` values on device `dev`; its address."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev:
+        if t.is_contiguous() and t.numel() >= count:
+            return t.data_ptr()
+    _refuse(fn, name, t, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    raise ValueError(f"{fn}: {name} holds {t.numel()} values, the call needs {count}")
+
+
+def _rows(fn: str, name: str, t, dtype, shape: tuple, row: int, dev: int) -> int:
+    """t: a `dtype` tensor of this shape whose rows (all dimensions but the first, `row` values) are
+    contiguous; its first dimension's stride."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+        if t.is_contiguous():
+            return row
+        stride = t.stride()
+        # a row's dimensions of one value may have any stride: those go the long way
+        if len(shape) == 2 and stride[1] == 1 or len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2]:
+            if stride[0] >= row:
+                return stride[0]
+    _refuse(fn, name, t, dtype, dev)
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
     want = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for n, s in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
         if n > 1 and s != want:
             raise ValueError(f"{fn}: {name} must have contiguous rows (strides {t.stride()})")
         want *= n
-    if t.shape[0] > 1 and t.stride(0) < want:
+    if shape[0] > 1 and t.stride(0) < want:
         raise ValueError(f"{fn}: {name}'s rows overlap (strides {t.stride()})")
-    _place(fn, name, t, dev)
-    return t.stride(0) if t.shape[0] > 1 else want
+    return t.stride(0) if shape[0] > 1 else want
 
 
 def _device(fn: str, name: str, t) -> int:
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        return torch.cuda.current_device()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor, not {type(t).__name__}")
-    if not t.is_cuda:
-        raise ValueError(f"{fn}: {name} must be a CUDA tensor, not on {t.device}")
-    return torch.cuda.current_device()
+    raise ValueError(f"{fn}: {name} must be a CUDA tensor, not on {t.device}")
 
 
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)  # current_stream() without making a Stream object
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _hand_over(stream, dev: int, *tensors) -> None:
+def _hand_over(stream, dev: int, tensors) -> None:
     """Tensors made here on the current stream and used on `stream`: their memory is not given out
     again before that stream is done with it."""
-    if stream is None:
-        return
     s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
     for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        t.record_stream(s)
 
 
 def _scale_bytes(rows: int, cols: int) -> int:
@@ -124,19 +133,19 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be 2-D, not {x.dim()}-D")
     rows, cols = x.shape
-    ld_x = _rows(fn, "x", x, _BF16, (rows, cols), dev)
+    ld_x = _rows(fn, "x", x, _BF16, (rows, cols), cols, dev)
     w = _arg(fn, "weight", weight, _BF16, cols, dev)
     r = s = None
     ld_r = ld_s = cols
     made = []
     if residual is not None:
-        ld_r = _rows(fn, "residual", residual, _BF16, (rows, cols), dev)
+        ld_r = _rows(fn, "residual", residual, _BF16, (rows, cols), cols, dev)
         r = residual.data_ptr()
         if summed is None:
-            summed = torch.empty((rows, cols), dtype=_BF16, device=x.device)
+            summed = x.new_empty((rows, cols))
             made.append(summed)
         else:
-            ld_s = _rows(fn, "summed", summed, _BF16, (rows, cols), dev)
+            ld_s = _rows(fn, "summed", summed, _BF16, (rows, cols), cols, dev)
         s = summed.data_ptr()
         for name, t, ld in (("residual", residual, ld_r), ("x", x, ld_x)):
             lo, hi = t.data_ptr(), t.data_ptr() + ((rows - 1) * ld + cols) * 2
@@ -145,13 +154,13 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     elif summed is not None:
         raise ValueError(f"{fn}: summed is the sum with a residual, and there is none")
     if codes is None:
-        codes = torch.empty((rows, cols), dtype=_U8, device=x.device)
+        codes = x.new_empty((rows, cols), dtype=_U8)
         made.append(codes)
     else:
         _arg(fn, "codes", codes, _U8, rows * cols, dev)
     need = _scale_bytes(rows, cols // 32)
     if scales is None:
-        scales = torch.empty(need, dtype=_U8, device=x.device)
+        scales = x.new_empty(need, dtype=_U8)
         made.append(scales)
     else:
         _arg(fn, "scales", scales, _U8, need, dev)
@@ -159,7 +168,8 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
                               scales.data_ptr(), s, ld_s, _raw_stream(stream, dev))
     if st:
         _fail(fn, st)
-    _hand_over(stream, dev, *made)
+    if stream is not None:
+        _hand_over(stream, dev, made)
     return codes, scales, x if residual is None else summed
 
 
@@ -169,7 +179,7 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
     if x.dim() != 2:
         raise ValueError(f"{fn}: x must be 2-D, not {x.dim()}-D")
     M, K = x.shape
-    ld_x = _rows(fn, "x", x, _BF16 if x_scales is None else _U8, (M, K), dev)
+    ld_x = _rows(fn, "x", x, _BF16 if x_scales is None else _U8, (M, K), K, dev)
     xs = None if x_scales is None else _arg(fn, "x_scales", x_scales, _U8, _scale_bytes(M, K // 32), dev)
     if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 2:
         raise ValueError(f"{fn}: w_codes must be a 2-D codes tensor [N, K/2]")
@@ -181,9 +191,9 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
     ldy = N
     made = out is None
     if made:
-        out = torch.empty((M, N), dtype=_BF16, device=x.device)
+        out = x.new_empty((M, N), dtype=_BF16)
     else:
-        ldy = _rows(fn, "out", out, _BF16, (M, N), dev)
+        ldy = _rows(fn, "out", out, _BF16, (M, N), N, dev)
     if nv:
         st = _lib().nvfp4_matvec(x.data_ptr(), xs, M, K, ld_x, hadamard, w, ws, _arg(fn, "g_w", g_w, _F32, 1, dev),
                                  out.data_ptr(), N, ldy, _raw_stream(stream, dev))
@@ -192,8 +202,8 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
                                  _raw_stream(stream, dev))
     if st:
         _fail(fn, st)
-    if made:
-        _hand_over(stream, dev, out)
+    if made and stream is not None:
+        _hand_over(stream, dev, (out,))
     return out
 
 
@@ -233,7 +243,7 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
     if block_table.dim() != 2:
         raise ValueError(f"{fn}: block_table must be 2-D, not {block_table.dim()}-D")
     B, width = block_table.shape
-    ld = _rows(fn, "block_table", block_table, _I32, (B, width), dev)
+    ld = _rows(fn, "block_table", block_table, _I32, (B, width), width, dev)
     pl = _arg(fn, "lens", lens, _I32, B, dev)
     pn = _arg(fn, "new_lens", new_lens, _I32, B, dev)
     pf = _arg(fn, "free_pages", free_pages, _I32, 1, dev)
@@ -242,17 +252,17 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
     if max_tokens < 1:
         raise ValueError(f"{fn}: max_tokens must be at least 1, not {max_tokens}")
     if cu_new is None:
-        cu_new = torch.empty(B + 1, dtype=_I32, device=block_table.device)
+        cu_new = block_table.new_empty(B + 1)
         made.append(cu_new)
     else:
         _arg(fn, "cu_new", cu_new, _I32, B + 1, dev)
     if slots is None:
-        slots = torch.empty(max_tokens, dtype=_I32, device=block_table.device)
+        slots = block_table.new_empty(max_tokens)
         made.append(slots)
     else:
         _arg(fn, "slots", slots, _I32, max_tokens, dev)
     if next_head is None:
-        next_head = torch.empty(1, dtype=_I32, device=block_table.device)
+        next_head = block_table.new_empty(1)
         made.append(next_head)
     else:
         _arg(fn, "next_head", next_head, _I32, 1, dev)
@@ -261,7 +271,8 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
                                 _raw_stream(stream, dev))
     if st:
         _fail(fn, st)
-    _hand_over(stream, dev, *made)
+    if stream is not None:
+        _hand_over(stream, dev, made)
     return cu_new, slots, next_head
 
 
@@ -292,8 +303,8 @@ def kv_fp8_store(k_new, v_new, slots, k_cache, v_cache, *, stream=None) -> None:
     if T < 1:
         raise ValueError(f"{fn}: slots must be a 1-D tensor of at least one slot")
     ps = _arg(fn, "slots", slots, _I32, T, dev)
-    ld_k = _rows(fn, "k_new", k_new, _BF16, (T, H, D), dev)
-    ld_v = _rows(fn, "v_new", v_new, _BF16, (T, H, D), dev)
+    ld_k = _rows(fn, "k_new", k_new, _BF16, (T, H, D), H * D, dev)
+    ld_v = _rows(fn, "v_new", v_new, _BF16, (T, H, D), H * D, dev)
     st = _lib().kv_fp8_store(k_new.data_ptr(), ld_k, v_new.data_ptr(), ld_v, ps, T, kc, ks, vc, vs, NP, H, P, D,
                              _raw_stream(stream, dev))
     if st:
@@ -318,16 +329,16 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
     if q.dim() != 3 or H < 1 or q.shape[1] % H or q.shape[2] != D:
         raise ValueError(f"{fn}: q must be [T, a multiple of {H} heads, {D}], not {list(q.shape)}")
     T, HQ = q.shape[0], q.shape[1]
-    ld_q = _rows(fn, "q", q, _BF16, (T, HQ, D), dev)
+    ld_q = _rows(fn, "q", q, _BF16, (T, HQ, D), HQ * D, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError(f"{fn}: block_table must be a 2-D tensor")
     B, width = block_table.shape
-    ld_t = _rows(fn, "block_table", block_table, _I32, (B, width), dev)
+    ld_t = _rows(fn, "block_table", block_table, _I32, (B, width), width, dev)
     pl = _arg(fn, "lens", lens, _I32, B, dev)
     pcu = _arg(fn, "cu_new", cu_new, _I32, B + 1, dev)
     made = []
     if out is None:
-        out = torch.empty((T, HQ, D), dtype=_BF16, device=q.device)
+        out = q.new_empty((T, HQ, D))
         made.append(out)
     else:
         _arg(fn, "out", out, _BF16, T * HQ * D, dev)
@@ -336,15 +347,16 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
         need = L.kv_fp8_attention_workspace_bytes(B, H, G, max_new, max_len, D)
         pw = None
         if need:
-            workspace = torch.empty(need, dtype=_U8, device=q.device)
+            workspace = q.new_empty(need, dtype=_U8)
             made.append(workspace)
             pw = workspace.data_ptr()
     else:
-        pw, need = _arg(fn, "workspace", workspace, workspace.dtype, 0, dev), workspace.numel() * workspace.element_size()
+        pw, need = _arg(fn, "workspace", workspace, getattr(workspace, "dtype", None), 0, dev), workspace.numel() * workspace.element_size()
     st = L.kv_fp8_attention(q.data_ptr(), ld_q, T, kc, ks, vc, vs, NP, P, block_table.data_ptr(), ld_t, width, pl, pcu,
                             max_new, max_len, D ** -0.5 if scale is None else scale, out.data_ptr(), B, H, G, D, pw,
                             need, _raw_stream(stream, dev))
     if st:
         _fail(fn, st)
-    _hand_over(stream, dev, *made)
+    if stream is not None:
+        _hand_over(stream, dev, made)
     return out
