@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
     const int k0 = blockIdx.x * a.chunk, kend = rq.len + imax + 1;  // keys the tile's last row sees
     if (k0 >= kend)
         return;
-    const int k1 = min(kend, k0 + a.chunk), held = rq.len + rq.n;  // rows behind `held` hold anything
+    const int k1 = min(kend, k0 + a.chunk);  // rows behind len + n hold anything, and are not read
     const int P1 = (1 << a.shift) - 1;
 
     for (int i = tid; i < (k1 - k0 + 15) / 16; i += KVP_THREADS) {
@@ -170,9 +170,11 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
     __syncthreads();
 
     uint32_t kr[2][2][KW], vr[2][4][VW];
-    auto row_ptr = [&](const uint8_t *codes, int key) {  // row `key` of this head; null where there is none
-        const int page = s_page[(key - k0) >> 4];
-        return page < 0 ? nullptr : codes + (((int64_t)page * a.H + h) << a.shift) * D + (int64_t)(key & P1) * D;
+    // row `key` of this head; go becomes false where there is no page
+    auto row_ptr = [&](const uint8_t *codes, int key, bool &go) {
+        const int page = go ? s_page[(key - k0) >> 4] : -1;
+        go = page >= 0;
+        return codes + (((int64_t)page * a.H + h) << a.shift) * D + (int64_t)(key & P1) * D;
     };
     auto load_k = [&](int kb) {
 #pragma unroll
@@ -180,10 +182,11 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int key = kb + 16 * u + 8 * e + g;
-                const uint8_t *p = key < k1 ? row_ptr(a.kc, key) : nullptr;
+                bool go = key < k1;
+                const uint8_t *p = row_ptr(a.kc, key, go);
 #pragma unroll
                 for (int w = 0; w < KW; w += 4) {
-                    const uint4 x = p ? ld_nc_v4(p + t * (D / 4) + 4 * w) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 x = ld_nc_v4_if(p + t * (D / 4) + 4 * w, go);
                     kr[u][e][w] = x.x;
                     kr[u][e][w + 1] = x.y;
                     kr[u][e][w + 2] = x.z;
@@ -197,15 +200,16 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = kb + 16 * u + 2 * t + (e & 1) + 8 * (e >> 1);
-                const uint8_t *p = key < k1 && key < held ? row_ptr(a.vc, key) : nullptr;
+                bool go = key < k1;
+                const uint8_t *p = row_ptr(a.vc, key, go);
                 if constexpr (VW == 4) {
-                    const uint4 x = p ? ld_nc_v4(p + g * 16) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 x = ld_nc_v4_if(p + g * 16, go);
                     vr[u][e][0] = x.x;
                     vr[u][e][1] = x.y;
                     vr[u][e][2] = x.z;
                     vr[u][e][3] = x.w;
                 } else {
-                    const uint2 x = p ? ld_nc_v2(p + g * 8) : make_uint2(0u, 0u);
+                    const uint2 x = ld_nc_v2_if(p + g * 8, go);
                     vr[u][e][0] = x.x;
                     vr[u][e][1] = x.y;
                 }

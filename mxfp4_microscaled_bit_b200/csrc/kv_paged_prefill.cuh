@@ -52,6 +52,15 @@ __device__ __forceinline__ void mma_f16_ts_w(uint32_t d, uint32_t a, uint64_t b,
                  : "memory");
 }
 
+// One arrival of a converged warp, which stays converged (a branch on the lane before the MMAs
+// makes their issue three times slower).
+__device__ __forceinline__ void mbar_arrive_w(uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
 // MN-major operand, 128-byte swizzle: rows (k) of 128 bytes = 64 values along MN, 8-row groups 1024
 // bytes apart (stride byte offset), the next 64 values `lbo` bytes on (leading byte offset).
 __device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo)
@@ -66,31 +75,26 @@ constexpr uint32_t kpp_idesc(int N, bool b_mn_major)
     return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(N / 8) << 17) | ((128u / 16u) << 24);
 }
 
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t *r)
+// 64 columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t *r)
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-                   "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
-                   "=r"(r[30]), "=r"(r[31])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%2"
+                 "5,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%4"
+                 "8,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                   "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+                   "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+                   "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+                   "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+                   "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+                   "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+                   "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+                   "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
                  : "r"(taddr)
-                 : "memory");
-}
-
-// Waits for this thread's tcgen05.ld; the registers go through it so that none is read before.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t *r)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
-                 :
                  : "memory");
 }
 
@@ -157,6 +161,28 @@ __device__ __forceinline__ void kpp_convert(uint8_t *base, int row, int cc, uint
         odd ? make_uint4(f[0], f[1], f[2], f[3]) : make_uint4(f[4], f[5], f[6], f[7]);
 }
 
+// The factor from a score's dot product to log2 units: 2^Xk times the row's.  Kept above 0, so that
+// the -inf of a masked score stays one.
+__device__ __forceinline__ float kpp_factor(float kf, float qs) { return fmaxf(kf * qs, 1.17549435e-38f); }
+
+// Scores of the row's columns behind `last` become -inf.
+__device__ __noinline__ void kpp_mask(uint32_t t_s, int last)
+{
+#pragma unroll 1
+    for (int k = 0; k < KPP_KEYS; k += 8) {
+        float v[8];
+        tmem_ld8(t_s + k, v);
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            r[j] = k + j > last ? 0xFF800000u : __float_as_uint(v[j]);
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t_s + k)
+                     : "memory");
+    }
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a, int min_rows)
 {
@@ -219,8 +245,9 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 m = fmaxf(m, finite_abs(f[j]));
         }
         const uint32_t e = m > 0.0f ? min(max(__float_as_uint(m) >> 23, 1u), 253u) : 127u;
-        const float inv = __uint_as_float((254u - e) << 23);
-        qs = __uint_as_float(e << 23) * a.qscale;
+        // a negative scale turns q around, so that the row's factor is not negative
+        const float inv = copysignf(__uint_as_float((254u - e) << 23), a.qscale);
+        qs = __uint_as_float(e << 23) * fabsf(a.qscale);
         for (int i = 0; i < D / 8; ++i) {
             float f[8];
             bf16x8_to_f32(mine ? ld_nc_v4(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), f);
@@ -252,75 +279,72 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     break;
                 tc_fence_after();
                 const int slot = i & (KPP_SLOTS - 1), k0 = i * KPP_KEYS;
-                const bool masked = k0 + KPP_KEYS - 1 > all || live < KPP_ROWS;
-                uint32_t s[2][32];  // two chunks of the row: one is worked on while the next arrives
-                // s' = log2(e) s + Xv, -inf where the row does not see the key
-                auto scale_chunk = [&](int k, uint32_t *v) {
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float f = ct.kf[slot][2 * k + g] * qs, x = ct.xv[slot][2 * k + g];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[16 * g + j] = __float_as_uint(fmaf(__uint_as_float(v[16 * g + j]), f, x));
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (k0 + 32 * k + j > lim)
-                                v[j] = 0xFF800000u;
-                    }
-                };
-                // the row is read twice, for its maximum and for its weights: held once, its 128 scores
-                // and their packing need more registers than sixteen warps have
+                if (k0 + KPP_KEYS - 1 > all || live < KPP_ROWS)
+                    kpp_mask(t_s, lim - k0);
+                // The row's largest s' = f s + Xv: f is positive and one for 16 keys, so it is that of the
+                // largest s.  The row does not fit the registers twice over; its upper half stays in
+                // them, the lower is read again for the weights.
+                uint32_t s[64];
                 float m = -INFINITY;
-                tmem_ld32_issue(t_s, s[0]);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    tmem_ld64(t_s + 64 * half, s);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    tmem_ld_wait(s[k & 1]);
-                    if (k < 3)
-                        tmem_ld32_issue(t_s + 32 * (k + 1), s[(k + 1) & 1]);
-                    scale_chunk(k, s[k & 1]);
+                    for (int g = 0; g < 4; ++g) {
+                        float top = max3f(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        m = max3f(m, __uint_as_float(s[k & 1][j]), __uint_as_float(s[k & 1][j + 1]));
+                        for (int j = 3; j < 15; j += 2)
+                            top = max3f(top, __uint_as_float(s[16 * g + j]), __uint_as_float(s[16 * g + j + 1]));
+                        top = fmaxf(top, __uint_as_float(s[16 * g + 15]));
+                        m = fmaxf(m, fmaf(top, kpp_factor(ct.kf[slot][4 * half + g], qs), ct.xv[slot][4 * half + g]));
+                    }
                 }
-                tmem_ld32_issue(t_s, s[0]);
                 float corr = 1.0f;
                 if (m > M + KPP_LAZY || (M == -INFINITY && m > M)) {
                     corr = ex2(M - m);  // 0 for the first keys
                     M = m;
                 }
-                if (__any_sync(0xffffffffu, corr != 1.0f) && i > 0) {
+                if (i > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
                     ok = warp_wait(&ct.odone[tile], (i - 1) & 1, abort, lane);
                     if (!ok)
                         break;
                     tc_fence_after();
-#pragma unroll 2
+#pragma unroll 1
                     for (int k = 0; k < D / 8; ++k)
                         tmem_scale8(t_o + 8 * k, corr);
                 }
                 den *= corr;
                 const float base = M == -INFINITY ? 0.0f : M;
+                // weights 2^(s' - M): the keys of the upper half go to columns 96 .., of the lower to 64 ..,
+                // all of them columns whose scores are in registers
+#pragma unroll 1
+                for (int half = 1; half >= 0; --half) {
+                    if (half == 0)
+                        tmem_ld64(t_s, s);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    tmem_ld_wait(s[k & 1]);
-                    if (k < 3)
-                        tmem_ld32_issue(t_s + 32 * (k + 1), s[(k + 1) & 1]);
-                    scale_chunk(k, s[k & 1]);
-                    uint32_t w[16];
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[16];
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float sum = 0.0f;
+                        for (int g = 0; g < 2; ++g) {
+                            const int grp = 4 * half + 2 * q + g;
+                            const float f = kpp_factor(ct.kf[slot][grp], qs), x = ct.xv[slot][grp] - base;
+                            const uint64_t f2 = f2_pack(f, f), x2 = f2_pack(x, x);
+                            uint64_t sum = 0ull;
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float w0 = ex2(__uint_as_float(s[k & 1][16 * g + j]) - base);
-                            const float w1 = ex2(__uint_as_float(s[k & 1][16 * g + j + 1]) - base);
-                            sum += w0 + w1;
-                            w[8 * g + j / 2] = cvt_f16x2(w0, w1);
+                            for (int j = 0; j < 16; j += 2) {
+                                const int e = 32 * q + 16 * g + j;
+                                float a0, a1;
+                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, x2), a0, a1);
+                                const float w0 = ex2(a0), w1 = ex2(a1);
+                                sum = f2_add(sum, f2_pack(w0, w1));
+                                w[8 * g + j / 2] = cvt_f16x2(w0, w1);
+                            }
+                            float s0, s1;
+                            f2_unpack(sum, s0, s1);
+                            den = fmaf(s0 + s1, ct.c[slot][grp], den);
                         }
-                        den = fmaf(sum, ct.c[slot][2 * k + g], den);
+                        tmem_st16(t_s + 64 + 32 * half + 16 * q, w);
                     }
-                    tmem_st16(t_s + 16 * k, w);  // columns that have been read already
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -333,9 +357,8 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     a.out + (int64_t)(rq.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_ld32_issue(t_o + 32 * k, o);
-                    tmem_ld_wait(o);
+                    float o[32];
+                    tmem_ld32(t_o + 32 * k, o);
                     if (mine)
 #pragma unroll
                         for (int j = 0; j < 32; j += 8) {
@@ -344,7 +367,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                             for (int e = 0; e < 4; ++e)
                                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
                                     : "=r"(y[e])
-                                    : "f"(__uint_as_float(o[j + 2 * e + 1]) * inv), "f"(__uint_as_float(o[j + 2 * e]) * inv));
+                                    : "f"(o[j + 2 * e + 1] * inv), "f"(o[j + 2 * e] * inv));
                             st_v4(dst + 32 * k + j, make_uint4(y[0], y[1], y[2], y[3]));
                         }
                 }
@@ -365,54 +388,71 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         constexpr int CPR = D / 16, RPP = 128 / CPR, PASSES = KPP_KEYS / RPP;  // 16-byte chunks a row, rows a pass
         const int u = tid - 256, cc = u % CPR, r0 = u / CPR;
         const int32_t *table = a.table + b * a.ld_t;
-        // lane g < 8 holds the page of the block's keys 16 g ..
-        auto pages_of = [&](int i) {
+        // Lane g holds what concerns the block's keys 16 (g % 8) ..: their page (-1: none) and its scale
+        // bytes.  Table entries are read two blocks ahead, scales and codes one, so that no load waits
+        // for another within a block.
+        auto entry_of = [&](int i) {
             const int key = i * KPP_KEYS + 16 * (lane & 7);
-            int page = -1;
-            if (key < kend) {
-                page = table[key >> a.shift];
-                if (page < 0 || page >= a.NP) {
-                    page = -1;
-                    report_error(FP4LIN_ERR_OUT_OF_RANGE);
-                }
-            }
-            return page;
+            return key < kend ? table[key >> a.shift] : -2;
         };
-        auto load = [&](const uint8_t *codes, int i, int pages, uint4 *x) {
+        auto page_of = [&](int entry) {
+            if (entry >= 0 && entry < a.NP)
+                return entry;
+            if (entry != -2 && lane < 8)
+                report_error(FP4LIN_ERR_OUT_OF_RANGE);
+            return -1;
+        };
+        // byte offset of this thread's chunk in each pass, -1 where there is no page; all shuffles
+        // together: one at a time, each waits its turn behind the tensor cores' use of shared memory
+        auto offsets = [&](int pages, int64_t *at) {
+            int page[PASSES];
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+                page[p] = __shfl_sync(0xffffffffu, pages, (r0 + p * RPP) >> 4);
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p)
+                at[p] = page[p] < 0 ? -1
+                                    : ((((int64_t)page[p] * a.H + h) << a.shift) + ((r0 + p * RPP) & P1)) * D + 16 * cc;
+        };
+        auto load = [&](const uint8_t *codes, int i, const int64_t *at, uint4 *x) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                const int row = r0 + p * RPP, key = i * KPP_KEYS + row;
-                const int page = __shfl_sync(0xffffffffu, pages, row >> 4);
-                x[p] = page >= 0 && key < kend
-                           ? ld_nc_v4(codes + ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D + 16 * cc)
-                           : make_uint4(0u, 0u, 0u, 0u);
+                const int key = i * KPP_KEYS + r0 + p * RPP;
+                x[p] = ld_nc_v4_if(codes + at[p], at[p] >= 0 && key < kend);
             }
         };
         uint4 xk[PASSES], xv[PASSES];
-        int pages = pages_of(0);
-        load(a.kc, 0, pages, xk);
-        load(a.vc, 0, pages, xv);
+        int pages = page_of(entry_of(0)), entry = entry_of(1);
+        uint32_t kbyte = pages >= 0 ? a.ks[(int64_t)pages * a.H + h] : 0u;
+        uint32_t vbyte = pages >= 0 ? a.vs[(int64_t)pages * a.H + h] : 0u;
+        int64_t at[PASSES];
+        offsets(pages, at);
+        load(a.kc, 0, at, xk);
+        load(a.vc, 0, at, xv);
         for (int i = 0; i < blocks; ++i) {
-            const int next = i + 1 < blocks ? pages_of(i + 1) : -1;
+            const int next = page_of(entry);
+            entry = entry_of(i + 2);
             const int st = i & 1, par = ((i >> 1) & 1) ^ 1;
             if (i >= 2 && !warp_wait(&ct.kfree[st], par, abort, lane))
                 break;
             if (warp == 8 && lane < 8) {
                 const int slot = i & (KPP_SLOTS - 1);
-                const uint32_t kb = pages >= 0 ? a.ks[(int64_t)pages * a.H + h] : 0u;
-                const uint32_t vb = pages >= 0 ? a.vs[(int64_t)pages * a.H + h] : 0u;
-                const float x = vb ? (float)((int)vb - 127) : KVP_ZERO_X;
-                ct.kf[slot][lane] = mxfp8_scale(kb);
+                const float x = vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X;
+                ct.kf[slot][lane] = mxfp8_scale(kbyte);
                 ct.xv[slot][lane] = pages >= 0 ? x : -INFINITY;
                 ct.c[slot][lane] = pages >= 0 ? ex2(-x) : 0.0f;
             }
+            kbyte = next >= 0 ? a.ks[(int64_t)next * a.H + h] : 0u;
+            vbyte = next >= 0 ? a.vs[(int64_t)next * a.H + h] : 0u;
 #pragma unroll
             for (int p = 0; p < PASSES; ++p)
                 kpp_convert<D>(s_k + st * TILE, r0 + p * RPP, cc, xk[p]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&ct.kfull[st]);
-            if (i + 1 < blocks)
-                load(a.kc, i + 1, next, xk);
+            if (i + 1 < blocks) {
+                offsets(next, at);
+                load(a.kc, i + 1, at, xk);
+            }
             if (i >= 2 && !warp_wait(&ct.vfree[st], par, abort, lane))
                 break;
             if ((i + 1) * KPP_KEYS - 1 > all) {  // keys that some rows do not see: weight 0 must stay 0
@@ -431,7 +471,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&ct.vfull[st]);
             if (i + 1 < blocks)
-                load(a.vc, i + 1, next, xv);
+                load(a.vc, i + 1, at, xv);
             pages = next;
         }
     } else {
@@ -445,18 +485,16 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     mma_f16_ss_w(tmem + j * 128, desc_sw128(qa + off), desc_sw128(ka + off), IQK, k > 0);
                 }
                 tc_commit_w(&ct.sfull[j]);
-                if (lane == 0)
-                    mbar_arrive(&ct.sfull[j]);  // passes on what kfull released (the page factors)
+                mbar_arrive_w(&ct.sfull[j]);  // passes on what kfull released (the page factors)
             };
             auto values = [&](int j, int i) {
                 const uint32_t va = smem_u32(s_v + (i & 1) * TILE);
 #pragma unroll
                 for (int k = 0; k < KPP_KEYS / 16; ++k)
-                    mma_f16_ts_w(tmem + 256 + j * D, tmem + j * 128 + 8 * k, desc_sw128_mn(va + k * 2048, KPP_KEYS * 128),
+                    mma_f16_ts_w(tmem + 256 + j * D, tmem + j * 128 + 64 + 8 * k, desc_sw128_mn(va + k * 2048, KPP_KEYS * 128),
                                  IPV, i > 0 || k > 0);
                 tc_commit_w(&ct.odone[j]);
-                if (lane == 0)
-                    mbar_arrive(&ct.odone[j]);  // and on what vfull released
+                mbar_arrive_w(&ct.odone[j]);  // and on what vfull released
             };
             bool ok = warp_poll(&ct.kfull[0], 0, abort, lane);
             if (ok) {

@@ -132,26 +132,22 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
     // this lane's two scale words: atom (tile, ct), row in_tile, words q0 and q0 + 1
     const uint8_t *sc = a.ws + (int64_t)tile * a.katoms_w * 512 + in_tile * 16 + q0 * 4;
 
+    // The scale bytes of 64 values from k on, rows A and B (MXFP4: in the low 16 bits, as 64 values are
+    // half of an atom's 4 columns).  Through L1: the neighbouring lanes' words share its sectors.
+    auto ld_scales = [&](int k, bool in) {
+        uint2 s = make_uint2(0u, 0u);
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0,%1}, [%2];\n\t}"
+                     : "+r"(s.x), "+r"(s.y)
+                     : "l"(sc + (int64_t)(k / (NV ? 64 : 128)) * 512), "r"((uint32_t)in));
+        return s;
+    };
+    auto half_of = [&](uint2 s) { return NV || !(t & 1) ? s : make_uint2(s.x >> 16, s.y >> 16); };
     auto load_w = [&](int c, uint32_t *ra, uint32_t *rb, uint2 &s) {
         const int k = c * MV_CHUNK + 64 * t;
         const bool in = c < c1 && k < a.K;
-        if (in && liveA)
-            ld_nc_32B(wA + k / 2, a.wide_w, ra);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                ra[i] = 0u;
-        if (in && liveB)
-            ld_nc_32B(wB + k / 2, a.wide_w, rb);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                rb[i] = 0u;
-        s = in ? *reinterpret_cast<const uint2 *>(sc + (int64_t)(k / (NV ? 64 : 128)) * 512) : make_uint2(0u, 0u);
-        if (!NV && (t & 1)) {  // 64 values are half of an atom's 4 columns
-            s.x >>= 16;
-            s.y >>= 16;
-        }
+        ld_nc_32B_if(wA + k / 2, a.wide_w, in && liveA, ra);
+        ld_nc_32B_if(wB + k / 2, a.wide_w, in && liveB, rb);
+        s = ld_scales(k, in);
     };
 
     float tot[NT][4];
@@ -210,15 +206,9 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
         if constexpr (!NV) {
             for (int c = sb; c < se; ++c) {
                 const int k = c * MV_CHUNK + 64 * t;
-                if (k < a.K) {
-                    uint2 s = *reinterpret_cast<const uint2 *>(sc + (int64_t)(k / 128) * 512);
-                    if (t & 1) {
-                        s.x >>= 16;
-                        s.y >>= 16;
-                    }
-                    refA = max(refA, max(s.x & 255u, (s.x >> 8) & 255u));
-                    refB = max(refB, max(s.y & 255u, (s.y >> 8) & 255u));
-                }
+                const uint2 s = half_of(ld_scales(k, k < a.K));
+                refA = max(refA, max(s.x & 255u, (s.x >> 8) & 255u));
+                refB = max(refB, max(s.y & 255u, (s.y >> 8) & 255u));
             }
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
@@ -231,7 +221,8 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-        auto multiply = [&](int c, const uint32_t *va, const uint32_t *vb, uint2 sw) {
+        auto multiply = [&](int c, const uint32_t *va, const uint32_t *vb, uint2 raw) {
+            const uint2 sw = half_of(raw);
             uint32_t sA[4], sB[4];  // f16x2 scales of the lane's 16-value quarters
             if constexpr (NV) {
                 uint32_t a01, a23, b01, b23;

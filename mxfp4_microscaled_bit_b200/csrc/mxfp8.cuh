@@ -13,6 +13,42 @@
 
 namespace fp4lin {
 
+// Loads under a predicate, zero where it is false.  The predicate is inside the asm: a branch around
+// a load makes the compiler wait for it before the next one is issued.
+__device__ __forceinline__ uint2 ld_nc_v2_if(const void *p, bool go)
+{
+    uint2 r = make_uint2(0u, 0u);
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+                 "@q ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n\t}"
+                 : "+r"(r.x), "+r"(r.y)
+                 : "l"(p), "r"((uint32_t)go));
+    return r;
+}
+
+__device__ __forceinline__ uint4 ld_nc_v4_if(const void *p, bool go)
+{
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "+r"(r.x), "+r"(r.y), "+r"(r.z), "+r"(r.w)
+                 : "l"(p), "r"((uint32_t)go));
+    return r;
+}
+
+// 32 bytes: one 256-bit load where `wide` (32-byte aligned), else two of 128.
+__device__ __forceinline__ void ld_nc_32B_if(const void *p, bool wide, bool go, uint32_t *r)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = 0u;
+    asm volatile("{\n\t.reg .pred w, n;\n\tsetp.ne.u32 w, %9, 0;\n\tsetp.ne.u32 n, %10, 0;\n\t"
+                 "@w ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "@n ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%8];\n\t"
+                 "@n ld.global.nc.L1::no_allocate.v4.b32 {%4,%5,%6,%7}, [%8+16];\n\t}"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 : "l"(p), "r"((uint32_t)(go && wide)), "r"((uint32_t)(go && !wide)));
+}
+
 // E8M0 byte of a block whose largest finite magnitude is amax (amax >= 0, finite).
 __device__ __forceinline__ uint32_t mxfp8_scale_byte(float amax)
 {
