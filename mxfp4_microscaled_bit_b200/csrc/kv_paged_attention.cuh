@@ -16,7 +16,7 @@
 #pragma once
 
 #include "gemm_sm100.cuh"
-#include "kv_attention.cuh"  // mma_16816x, f16x2_bits
+#include "kv_attention.cuh"  // mma_16816x
 #include "mxfp8.cuh"
 
 namespace fp4lin {
@@ -99,10 +99,10 @@ __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, u
     for (int i = 0; i < D / 32; ++i) {
         float f[8];
         bf16x8_to_f32(u[i], f);
-        qb[2 * i][0] = f16x2_bits(f[0] * inv, f[1] * inv);
-        qb[2 * i][1] = f16x2_bits(f[2] * inv, f[3] * inv);
-        qb[2 * i + 1][0] = f16x2_bits(f[4] * inv, f[5] * inv);
-        qb[2 * i + 1][1] = f16x2_bits(f[6] * inv, f[7] * inv);
+        qb[2 * i][0] = cvt_f16x2(f[0] * inv, f[1] * inv);
+        qb[2 * i][1] = cvt_f16x2(f[2] * inv, f[3] * inv);
+        qb[2 * i + 1][0] = cvt_f16x2(f[4] * inv, f[5] * inv);
+        qb[2 * i + 1][1] = cvt_f16x2(f[6] * inv, f[7] * inv);
     }
     return __uint_as_float(e << 23);
 }
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                wb[u][nt][0] = movmatrix(f16x2_bits(s[u][nt][0], s[u][nt][1]));
-                wb[u][nt][1] = movmatrix(f16x2_bits(s[u][nt][2], s[u][nt][3]));
+                wb[u][nt][0] = movmatrix(cvt_f16x2(s[u][nt][0], s[u][nt][1]));
+                wb[u][nt][1] = movmatrix(cvt_f16x2(s[u][nt][2], s[u][nt][3]));
             }
         }
 #pragma unroll

@@ -126,13 +126,6 @@ __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f)
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Bytes of w that are the E4M3 NaN code become 0; true if there was one.
 __device__ __forceinline__ bool drop_nan_codes(uint32_t &w)
 {

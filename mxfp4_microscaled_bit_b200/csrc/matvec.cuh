@@ -8,29 +8,34 @@
 // goes from a 256-bit load to a tensor-core fragment in registers: E2M1 times its scale is exact
 // in f16 (at most 6 bits), so the scale costs one f16x2 multiply a pair and the product accumulates
 // in binary32 over the whole slice of K.  Exponents that f16 cannot hold are taken out first:
-//   x: scaled by a power of two (a row's largest magnitude in the slice lands in [2^14, 2^15));
+//   x: scaled by a power of two (a row's largest magnitude in 256 values lands in [2^14, 2^15));
 //      what is below 2^-39 of that maximum is lost, less than binary32 sums resolve;
-//   MXFP4 scales: relative to the row's largest in the segment; blocks more than 2^24 below it
-//      lose bits that the sum could not hold either.
+//   MXFP4 scales: relative to the row's largest in 256 values; blocks more than 2^24 below it lose
+//      bits that the sum could not hold either.
 // Rotated activations are rounded to f16 once (2^-11 relative steps, against bf16 outputs).
 //
-// A CTA takes 128 weight rows and a slice of K; the CTAs of one row tile form a cluster (at most 8)
-// and add their sums through distributed shared memory in a fixed order: one launch, no workspace,
-// the same bits every time.
+// What it takes to come near HBM's rate with so few bytes is little to wait for before the weights are
+// asked for, and little to do for each.  A CTA takes 128 weight rows, 16 a warp, and a slice of K; the
+// CTAs that share rows form a cluster (at most 8) along K.  The partial sums of a row go to one CTA of
+// the cluster through distributed shared memory and are added in a fixed order: one launch, no
+// workspace, the same bits every time.
 #pragma once
 
 #include <cooperative_groups.h>
 
-#include "kv_attention.cuh"  // mma_16816x, f16x2_bits
+#include "kv_attention.cuh"  // mma_16816x
+#include "kv_paged.cuh"      // f16x2_pow2_neg
 #include "mxfp8.cuh"
 #include "quantize.cuh"
 
 namespace fp4lin {
 
 constexpr int MV_THREADS = 256;
-constexpr int MV_ROWS = 128;       // weight rows a CTA: 8 warps x 16
+constexpr int MV_WARPS = MV_THREADS / 32;
+constexpr int MV_ROWS = 128;       // rows of the scale layout's tiles: 8 groups of 16
 constexpr int MV_CHUNK = 256;      // k a warp step: 64 consecutive values a lane and row
-constexpr int MV_SEG = 8;          // chunks a segment: x and the scales are normalised once per segment
+constexpr int MV_SEG = 8;          // chunks of x that a CTA holds at a time
+constexpr int MV_DEPTH = 2;        // chunks of weights that a warp has in flight
 constexpr int MV_MAX_M = 16;
 
 struct MatvecShape {
@@ -41,49 +46,98 @@ struct MatvecShape {
     __nv_bfloat16 *y;
     int64_t ld_x, ldy, katoms_w, katoms_x;
     int M, N, K, nchunks, per_cta; // per_cta: chunks a CTA of the cluster takes
-    bool wide_w, wide_x;
+    int mp_shift;                  // 1 << mp_shift: M rounded up to a power of two, at most 8
+    bool wide_w;
 };
 
-// Shared memory: a segment's x as B fragments (16 bytes for 8 consecutive k of one row), the
-// per-row exponents, and the CTA's sums.
-constexpr size_t mv_smem(int M, int chunks)
+// Shared memory: a segment's x as B fragments (16 bytes for 8 consecutive k of one row) with the
+// scale of each (chunk, row), and the partial sums that the cluster's warps send this CTA.
+constexpr size_t mv_smem(int M, int chunks, int ranks)
 {
-    return (size_t)chunks * MV_CHUNK * M * 2 + MV_MAX_M * 4 + (size_t)MV_ROWS * M * 4;
+    return (size_t)chunks * MV_CHUNK * M * 2 + MV_SEG * MV_MAX_M * 4 + (size_t)ranks * M * ((MV_ROWS + ranks - 1) / ranks) * 4;
 }
 
-// 32 consecutive values of row m at column k as binary32, rotated where asked.
+// A lane's share of a (row, chunk) of x: 8 consecutive values, raw.
+struct MvRaw {
+    uint4 v;        // bf16; MXFP8: codes in x, y
+    uint32_t byte;  // MXFP8: the block's scale
+};
+
+// x and xs point at this lane's share of chunk 0.
+template <bool X8>
+__device__ __forceinline__ MvRaw mv_load_x(const uint8_t *x, const uint8_t *xs, int c, bool go)
+{
+    MvRaw r;
+    r.byte = 0u;
+    if constexpr (X8) {
+        const uint2 v = ld_nc_v2_if(x + c * MV_CHUNK, go);
+        r.v = make_uint4(v.x, v.y, 0u, 0u);
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u8 %0, [%1];\n\t}"
+                     : "+r"(r.byte)
+                     : "l"(xs + c * 1024), "r"((uint32_t)go));  // 8 columns of the scale layout are two atoms
+    } else {
+        r.v = ld_nc_v4_if(x + c * (MV_CHUNK * 2), go);
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The power of two that takes a magnitude with these binary32 bits to [2^14, 2^15), and its inverse;
+// both stay normal.
+__device__ __forceinline__ uint32_t mv_exponent(uint32_t top) { return top ? min(max(top >> 23, 15u), 253u) : 141u; }
+__device__ __forceinline__ float mv_inverse(uint32_t top) { return __uint_as_float((268u - mv_exponent(top)) << 23); }
+__device__ __forceinline__ float mv_scale(uint32_t top) { return __uint_as_float((mv_exponent(top) - 14u) << 23); }
+
+// A (row, chunk) of x, 8 values a lane, as f16 fragments (f) under one power of two (returned).  The
+// whole warp calls it.  MXFP8: the codes, exact in f16, relative to the chunk's largest scale.
+// bf16: relative to the largest magnitude, rotated first where asked (a rotation's block is 2 or 4
+// lanes' values).
 template <bool X8, int HAD>
-__device__ __forceinline__ void mv_load_x(const MatvecShape &a, int m, int k, float *v)
+__device__ __forceinline__ float mv_stage(const MvRaw &r, int lane, uint4 &f)
 {
     if constexpr (X8) {
-        const uint8_t *p = static_cast<const uint8_t *>(a.x) + m * a.ld_x + k;
-        const float s = mxfp8_scale(a.xs[tc_offset(m, k / 32, a.katoms_x)]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p + 16 * i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t lo, hi;
-                e4m3x4_to_f16(w[j], lo, hi);
-                const float2 p0 = half2_to_float2(lo), p1 = half2_to_float2(hi);
-                v[16 * i + 4 * j] = p0.x * s;
-                v[16 * i + 4 * j + 1] = p0.y * s;
-                v[16 * i + 4 * j + 2] = p1.x * s;
-                v[16 * i + 4 * j + 3] = p1.y * s;
-            }
-        }
+        const uint32_t ref = __reduce_max_sync(0xffffffffu, r.byte), s = f16x2_pow2_neg((int)(ref - r.byte));
+        uint32_t h[4];
+        e4m3x4_to_f16(r.v.x, h[0], h[1]);
+        e4m3x4_to_f16(r.v.y, h[2], h[3]);
+        f = make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));
+        return mxfp8_scale(ref);
     } else {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.x) + m * a.ld_x + k;
+        float v[8];
+        bf16x8_to_f32(r.v, v);
+        uint32_t top;
+        if constexpr (HAD == 0) {
+            const uint32_t m = 0x7FFF7FFFu;  // magnitudes; a NaN is passed over
+            const uint32_t t2 = max_bf16x2(max_bf16x2(r.v.x & m, r.v.y & m), max_bf16x2(r.v.z & m, r.v.w & m));
+            top = max(t2 << 16, t2 & 0xFFFF0000u);
+        } else {
+            fwht<8>(v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            bf16x8_to_f32(*reinterpret_cast<const uint4 *>(p + 8 * i), v + 8 * i);
-        if constexpr (HAD == 16) {
-            fwht_scaled_packed<16>(v, 0.25f);
-            fwht_scaled_packed<16>(v + 16, 0.25f);
-        } else if constexpr (HAD == 32) {
-            fwht_scaled_packed<32>(v, __uint_as_float(0x3E3504F3u));
+            for (int o = 1; o < HAD / 8; o <<= 1)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float w = __shfl_xor_sync(0xffffffffu, v[j], o);
+                    v[j] = lane & o ? __fsub_rn(w, v[j]) : __fadd_rn(v[j], w);
+                }
+            float t = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = __fmul_rn(v[j], HAD == 16 ? 0.25f : __uint_as_float(0x3E3504F3u));
+                t = fmaxf(t, fabsf(v[j]));
+            }
+            top = __float_as_uint(t);
         }
+        top = __reduce_max_sync(0xffffffffu, top);  // bits in order, as no magnitude is negative
+        const float inv = mv_inverse(top);
+        f = make_uint4(cvt_f16x2(v[0] * inv, v[1] * inv), cvt_f16x2(v[2] * inv, v[3] * inv),
+                       cvt_f16x2(v[4] * inv, v[5] * inv), cvt_f16x2(v[6] * inv, v[7] * inv));
+        return mv_scale(top);
     }
 }
 
@@ -100,16 +154,20 @@ __device__ __forceinline__ void mv_weights(uint32_t w, uint32_t s, uint32_t *h)
         : "r"(w), "r"(s));
 }
 
-// f16x2 of 2^-d for d >= 0: 0 from 25 on.
-__device__ __forceinline__ uint32_t mv_pow2_neg(uint32_t d)
-{
-    const uint32_t h = d <= 14u ? (15u - d) << 10 : d <= 24u ? 1u << (24u - d) : 0u;
-    return h | (h << 16);
-}
+// n / d for n * d < 2^20 by a reciprocal (n up to 2048 here, d up to 128): 2^20/d rounded up is off by
+// less than d/2^20 of 1/d.
+struct SmallDiv {
+    uint32_t inv;
+    __device__ __forceinline__ explicit SmallDiv(int d) : inv((1u << 20) / (uint32_t)d + 1u) {}
+    __device__ __forceinline__ int operator()(int n) const { return (int)(((uint32_t)n * inv) >> 20); }
+};
 
-// One warp: 16 weight rows.  MMA row p (0..15) is the tile's row 32 q + 4 warp + i with i = p % 4 and
-// q = 2 (p/4 % 2) + p/8: a lane's two rows (p = g and g + 8) then have neighbouring words in a scale
-// atom, and the warp's scale bytes fill whole 64-byte runs.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// One warp: 16 weight rows.  MMA row p (0..15) of row group w is the 128-row tile's row 32 q + 4 w + i
+// with i = p % 4 and q = 2 (p/4 % 2) + p/8: a lane's two rows (p = g and g + 8) then have neighbouring
+// words in a scale atom, and the warp's scale bytes fill whole 64-byte runs.
 template <bool NV, bool X8, int HAD, int NT>
 __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
 {
@@ -119,11 +177,13 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int rank = (int)cl.block_rank(), ranks = (int)cl.num_blocks();
     const int tile = blockIdx.x / ranks;
+    const SmallDiv by_ranks(ranks);
     const int c0 = rank * a.per_cta, c1 = min(c0 + a.per_cta, a.nchunks);
-    uint4 *s_x = reinterpret_cast<uint4 *>(mv_dyn);
     const int seg_chunks = min(a.per_cta, MV_SEG);
-    float *s_scale = reinterpret_cast<float *>(mv_dyn + (size_t)seg_chunks * MV_CHUNK * a.M * 2);
-    float *s_y = s_scale + MV_MAX_M;  // [M][128]
+    uint4 *s_x = reinterpret_cast<uint4 *>(mv_dyn);
+    float *s_xs = reinterpret_cast<float *>(mv_dyn + (size_t)seg_chunks * MV_CHUNK * a.M * 2);  // [chunk][MV_MAX_M]
+    float *s_y = s_xs + MV_SEG * MV_MAX_M;           // [source rank][M][rows of this rank]
+    const int own = (MV_ROWS + ranks - 1) / ranks;  // the CTA's row n is rank n % ranks'
 
     const int q0 = 2 * (g >> 2), in_tile = 4 * warp + (g & 3);
     const int rowA = tile * MV_ROWS + 32 * q0 + in_tile, rowB = rowA + 32;
@@ -132,98 +192,79 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
     // this lane's two scale words: atom (tile, ct), row in_tile, words q0 and q0 + 1
     const uint8_t *sc = a.ws + (int64_t)tile * a.katoms_w * 512 + in_tile * 16 + q0 * 4;
 
-    // The scale bytes of 64 values from k on, rows A and B (MXFP4: in the low 16 bits, as 64 values are
-    // half of an atom's 4 columns).  Through L1: the neighbouring lanes' words share its sectors.
-    auto ld_scales = [&](int k, bool in) {
-        uint2 s = make_uint2(0u, 0u);
+    // s: the scale bytes of 64 values of rows A and B (MXFP4: two of an atom's 4 columns).  Through L1,
+    // as the neighbouring lanes' words share its sectors.
+    auto load_w = [&](int c, bool go, uint32_t *ra, uint32_t *rb, uint2 &s) {
+        const int k = c * MV_CHUNK + 64 * t;
+        go = go && k < a.K;
+        ld_nc_32B_if(wA + k / 2, a.wide_w, go && liveA, ra);
+        ld_nc_32B_if(wB + k / 2, a.wide_w, go && liveB, rb);
+        s = make_uint2(0u, 0u);
         asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0,%1}, [%2];\n\t}"
                      : "+r"(s.x), "+r"(s.y)
-                     : "l"(sc + (int64_t)(k / (NV ? 64 : 128)) * 512), "r"((uint32_t)in));
-        return s;
-    };
-    auto half_of = [&](uint2 s) { return NV || !(t & 1) ? s : make_uint2(s.x >> 16, s.y >> 16); };
-    auto load_w = [&](int c, uint32_t *ra, uint32_t *rb, uint2 &s) {
-        const int k = c * MV_CHUNK + 64 * t;
-        const bool in = c < c1 && k < a.K;
-        ld_nc_32B_if(wA + k / 2, a.wide_w, in && liveA, ra);
-        ld_nc_32B_if(wB + k / 2, a.wide_w, in && liveB, rb);
-        s = ld_scales(k, in);
+                     : "l"(sc + (int64_t)(k / (NV ? 64 : 128)) * 512), "r"((uint32_t)go));
     };
 
+    // the row of x that this lane's fragments come from: one behind the last repeats it (its sums are dropped)
+    int xrow[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        xrow[nt] = min(8 * nt + g, a.M - 1);
     float tot[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         tot[nt][0] = tot[nt][1] = tot[nt][2] = tot[nt][3] = 0.0f;
     pdl_wait();
-    const float gw = NV ? *a.g : 1.0f;
+    cluster_arrive();  // completed before a CTA writes into another: by then all have started
     for (int sb = c0; sb < c1; sb += MV_SEG) {
         const int se = min(sb + MV_SEG, c1);
-        uint32_t wa[2][8], wb[2][8];
-        uint2 ws[2];
-        load_w(sb, wa[0], wb[0], ws[0]);
-        // stage x: largest magnitude per row, then f16 fragments
-        const int kb = sb * MV_CHUNK, kn = min(se * MV_CHUNK, a.K) - kb, blocks = kn / 32;
-        __syncthreads();  // the previous segment's fragments are done with
-        for (int m = warp; m < a.M; m += MV_THREADS / 32) {
-            float top = 0.0f;
-            for (int i = lane; i < blocks; i += 32) {
-                float v[32];
-                mv_load_x<X8, HAD>(a, m, kb + 32 * i, v);
+        // Stage x while the weights are on their way.  A warp has a row of x (two where M > 8) and every
+        // 8/Mp-th chunk of it, Mp = M rounded up to a power of two, at most 8; BATCH chunks are loaded
+        // together.  A chunk's largest magnitude is the warp's own business.
+        constexpr int BATCH = 4;
+        const int xm = warp & ((1 << a.mp_shift) - 1), xc = warp >> a.mp_shift, xstep = MV_WARPS >> a.mp_shift;
+        const int chunks = se - sb, xk = sb * MV_CHUNK + 8 * lane;
+        MvRaw raw[BATCH];
+        auto load_x = [&](int m, int c) {
+            const uint8_t *x = static_cast<const uint8_t *>(a.x) + (m * a.ld_x + xk) * (X8 ? 1 : 2);
+            const uint8_t *xs = X8 ? a.xs + tc_offset(m, xk / 32, a.katoms_x) : nullptr;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    top = fmaxf(top, finite_abs(v[j]));
+            for (int b = 0; b < BATCH; ++b) {
+                const int cb = c + b * xstep;
+                raw[b] = mv_load_x<X8>(x, xs, cb, m < a.M && cb < chunks && xk + cb * MV_CHUNK < a.K);
             }
+        };
+        load_x(xm, xc);
+        uint32_t wa[MV_DEPTH][8], wb[MV_DEPTH][8];
+        uint2 ws[MV_DEPTH];
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // 2^(14 - e), e the exponent of `top`; both it and its inverse stay normal
-            const uint32_t e = top > 0.0f ? min(max(__float_as_uint(top) >> 23, 15u), 253u) : 141u;
-            const float inv = __uint_as_float((268u - e) << 23);
-            if (lane == 0)
-                s_scale[m] = __uint_as_float((e - 14u) << 23);
-            for (int i = lane; i < (se - sb) * (MV_CHUNK / 32); i += 32) {
-                float v[32];
-                if (i < blocks)
-                    mv_load_x<X8, HAD>(a, m, kb + 32 * i, v);
-                else
+        for (int d = 0; d < MV_DEPTH; ++d)
+            load_w(sb + d, sb + d < se, wa[d], wb[d], ws[d]);
+        __syncthreads();  // the last segment's fragments are done with
+#pragma unroll 1
+        for (int m = xm; m < a.M; m += 8) {
+            uint4 *to = s_x + ((lane & 7) * a.M + m) * 4 + (lane >> 3);  // word lane % 8 of lane slot t = lane / 8
+#pragma unroll 1
+            for (int c = xc; c < chunks; c += BATCH * xstep) {
+                if (m != xm || c != xc)
+                    load_x(m, c);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = 0.0f;
-                // chunk i/8, lane slot t = (i/2)%4, words 4*(i%2) .. +3
-                const int c = i >> 3, tt = (i >> 1) & 3, w0 = 4 * (i & 1);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint4 f;
-                    f.x = f16x2_bits(v[8 * w] * inv, v[8 * w + 1] * inv);
-                    f.y = f16x2_bits(v[8 * w + 2] * inv, v[8 * w + 3] * inv);
-                    f.z = f16x2_bits(v[8 * w + 4] * inv, v[8 * w + 5] * inv);
-                    f.w = f16x2_bits(v[8 * w + 6] * inv, v[8 * w + 7] * inv);
-                    s_x[((c * 8 + w0 + w) * a.M + m) * 4 + tt] = f;
+                for (int b = 0; b < BATCH; ++b) {
+                    const int cb = c + b * xstep;
+                    if (cb < chunks) {
+                        uint4 f;
+                        const float scale = mv_stage<X8, HAD>(raw[b], lane, f);
+                        to[cb * 32 * a.M] = f;
+                        if (lane == 0)
+                            s_xs[cb * MV_MAX_M + m] = scale;
+                    }
                 }
             }
         }
-        uint32_t refA = 0u, refB = 0u;  // MXFP4: the rows' largest scale bytes in the segment
-        if constexpr (!NV) {
-            for (int c = sb; c < se; ++c) {
-                const int k = c * MV_CHUNK + 64 * t;
-                const uint2 s = half_of(ld_scales(k, k < a.K));
-                refA = max(refA, max(s.x & 255u, (s.x >> 8) & 255u));
-                refB = max(refB, max(s.y & 255u, (s.y >> 8) & 255u));
-            }
-#pragma unroll
-            for (int o = 1; o <= 2; o <<= 1) {
-                refA = max(refA, __shfl_xor_sync(0xffffffffu, refA, o));
-                refB = max(refB, __shfl_xor_sync(0xffffffffu, refB, o));
-            }
-        }
         __syncthreads();
-        float acc[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-        auto multiply = [&](int c, const uint32_t *va, const uint32_t *vb, uint2 raw) {
-            const uint2 sw = half_of(raw);
+        auto multiply = [&](int c, const uint32_t *va, const uint32_t *vb, uint2 sw) {
             uint32_t sA[4], sB[4];  // f16x2 scales of the lane's 16-value quarters
+            float fA = 1.0f, fB = 1.0f;
             if constexpr (NV) {
                 uint32_t a01, a23, b01, b23;
                 e4m3x4_to_f16(sw.x, a01, a23);
@@ -237,11 +278,34 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                 sB[2] = __byte_perm(b23, b23, 0x1010);
                 sB[3] = __byte_perm(b23, b23, 0x3232);
             } else {
-                sA[0] = sA[1] = mv_pow2_neg(refA - (sw.x & 255u));
-                sA[2] = sA[3] = mv_pow2_neg(refA - ((sw.x >> 8) & 255u));
-                sB[0] = sB[1] = mv_pow2_neg(refB - (sw.y & 255u));
-                sB[2] = sB[3] = mv_pow2_neg(refB - ((sw.y >> 8) & 255u));
+                if (t & 1) {  // 64 values are half of an atom's 4 columns
+                    sw.x >>= 16;
+                    sw.y >>= 16;
+                }
+                const uint32_t a0 = sw.x & 255u, a1 = (sw.x >> 8) & 255u, b0 = sw.y & 255u, b1 = (sw.y >> 8) & 255u;
+                uint32_t refA = max(a0, a1), refB = max(b0, b1);  // the rows' largest in the chunk
+#pragma unroll
+                for (int o = 1; o <= 2; o <<= 1) {
+                    refA = max(refA, __shfl_xor_sync(0xffffffffu, refA, o));
+                    refB = max(refB, __shfl_xor_sync(0xffffffffu, refB, o));
+                }
+                sA[0] = sA[1] = f16x2_pow2_neg((int)(refA - a0));
+                sA[2] = sA[3] = f16x2_pow2_neg((int)(refA - a1));
+                sB[0] = sB[1] = f16x2_pow2_neg((int)(refB - b0));
+                sB[2] = sB[3] = f16x2_pow2_neg((int)(refB - b1));
+                fA = mxfp8_scale(refA);
+                fB = mxfp8_scale(refB);
             }
+            // several sums side by side: an MMA that waits for the last one's takes four times as long
+            constexpr int CHAINS = NT == 1 ? 4 : 2;
+            float acc[CHAINS][NT][4];
+#pragma unroll
+            for (int q = 0; q < CHAINS; ++q)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.0f;
+            const uint4 *xc = s_x + (c - sb) * 32 * a.M + t;
+            const int step = 4 * a.M;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t ha[4], hb[4];
@@ -249,55 +313,66 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                 mv_weights(vb[i], sB[i >> 1], hb);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const int m = 8 * nt + g;
-                    const uint4 f = m < a.M ? s_x[(((c - sb) * 8 + i) * a.M + m) * 4 + t] : make_uint4(0u, 0u, 0u, 0u);
-                    mma_16816x(acc[nt], ha[0], hb[0], ha[1], hb[1], f.x, f.y);
-                    mma_16816x(acc[nt], ha[2], hb[2], ha[3], hb[3], f.z, f.w);
+                    const uint4 f = xc[i * step + 4 * xrow[nt]];
+                    mma_16816x(acc[(2 * i) % CHAINS][nt], ha[0], hb[0], ha[1], hb[1], f.x, f.y);
+                    mma_16816x(acc[(2 * i + 1) % CHAINS][nt], ha[2], hb[2], ha[3], hb[3], f.z, f.w);
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // columns 2t, 2t+1 of the token tile; rows A, A, B, B
+                    float sum = acc[0][nt][e] + acc[1][nt][e];
+                    if constexpr (CHAINS == 4)
+                        sum += acc[2][nt][e] + acc[3][nt][e];
+                    const float xs = s_xs[(c - sb) * MV_MAX_M + 8 * nt + 2 * t + (e & 1)];
+                    tot[nt][e] = NV ? fmaf(sum, xs, tot[nt][e]) : fmaf(sum * xs, e < 2 ? fA : fB, tot[nt][e]);
+                }
         };
-        for (int c = sb; c < se; c += 2) {
-            if (c + 1 < se)
-                load_w(c + 1, wa[1], wb[1], ws[1]);
-            multiply(c, wa[0], wb[0], ws[0]);
-            if (c + 1 < se) {
-                if (c + 2 < se)
-                    load_w(c + 2, wa[0], wb[0], ws[0]);
-                multiply(c + 1, wa[1], wb[1], ws[1]);
+#pragma unroll 1
+        for (int c = sb; c < se; c += MV_DEPTH) {
+#pragma unroll
+            for (int d = 0; d < MV_DEPTH; ++d) {
+                if (c + d < se) {
+                    multiply(c + d, wa[d], wb[d], ws[d]);
+                    if (c + d + MV_DEPTH < se)
+                        load_w(c + d + MV_DEPTH, true, wa[d], wb[d], ws[d]);
+                }
             }
         }
-        const float fA = NV ? gw : mxfp8_scale(refA), fB = NV ? gw : mxfp8_scale(refB);
+    }
+    // each row's share goes to the CTA that sums it
+    cluster_wait();
+    {
+        const int nA = 16 * warp + g, nB = nA + 8;  // rows in the CTA's own order: a warp's 16 MMA rows
+        const int slot = rank * a.M * own;
+        float *toA = cl.map_shared_rank(s_y, nA - by_ranks(nA) * ranks) + slot + by_ranks(nA);
+        float *toB = cl.map_shared_rank(s_y, nB - by_ranks(nB) * ranks) + slot + by_ranks(nB);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {  // columns 2t, 2t+1 of the token tile
+            for (int e = 0; e < 2; ++e) {
                 const int m = 8 * nt + 2 * t + e;
-                const float xs = m < a.M ? s_scale[m] : 0.0f;
-                tot[nt][e] = fmaf(acc[nt][e] * xs, fA, tot[nt][e]);
-                tot[nt][e + 2] = fmaf(acc[nt][e + 2] * xs, fB, tot[nt][e + 2]);
+                if (m < a.M) {
+                    toA[m * own] = tot[nt][e];
+                    toB[m * own] = tot[nt][e + 2];
+                }
             }
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = 8 * nt + 2 * t + e;
-            if (m < a.M) {
-                s_y[m * MV_ROWS + 32 * q0 + in_tile] = tot[nt][e];
-                s_y[m * MV_ROWS + 32 * q0 + 32 + in_tile] = tot[nt][e + 2];
-            }
-        }
-    cl.sync();
-    // this CTA's share of the tile's outputs: rows rank, rank + ranks, .. of M * 128 / 32 groups of 32
-    for (int i = rank * 32 + (tid & 31) + (tid >> 5) * 32 * ranks; i < a.M * MV_ROWS; i += ranks * MV_THREADS) {
+    cluster_arrive();
+    cluster_wait();
+    const float gw = NV ? *a.g : 1.0f;
+    const SmallDiv by_own(own);
+    for (int i = tid; i < a.M * own; i += MV_THREADS) {
+        const int m = by_own(i), n = (i - m * own) * ranks + rank;
         float sum = 0.0f;
-        for (int r = 0; r < ranks; ++r)
-            sum += *cl.map_shared_rank(s_y + i, r);
-        const int m = i / MV_ROWS, n = tile * MV_ROWS + (i - m * MV_ROWS);
-        if (n < a.N)
-            a.y[m * a.ldy + n] = __float2bfloat16_rn(sum);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            sum += r < ranks ? s_y[r * a.M * own + i] : 0.0f;
+        const int p = n & 15, row = tile * MV_ROWS + 32 * (2 * ((p >> 2) & 1) + (p >> 3)) + 4 * (n >> 4) + (p & 3);
+        if (n < MV_ROWS && row < a.N)
+            a.y[m * a.ldy + row] = __float2bfloat16_rn(sum * gw);
     }
-    cl.sync();  // no CTA leaves while its sums are read
 }
 
 }  // namespace fp4lin

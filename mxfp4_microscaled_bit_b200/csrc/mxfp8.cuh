@@ -35,18 +35,25 @@ __device__ __forceinline__ uint4 ld_nc_v4_if(const void *p, bool go)
     return r;
 }
 
-// 32 bytes: one 256-bit load where `wide` (32-byte aligned), else two of 128.
+// 32 bytes: one 256-bit load where `wide` (32-byte aligned), else two of 128.  Not both under
+// predicates: even one that is off would wait for the registers of the other.
 __device__ __forceinline__ void ld_nc_32B_if(const void *p, bool wide, bool go, uint32_t *r)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         r[i] = 0u;
-    asm volatile("{\n\t.reg .pred w, n;\n\tsetp.ne.u32 w, %9, 0;\n\tsetp.ne.u32 n, %10, 0;\n\t"
-                 "@w ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                 "@n ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%8];\n\t"
-                 "@n ld.global.nc.L1::no_allocate.v4.b32 {%4,%5,%6,%7}, [%8+16];\n\t}"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                 : "l"(p), "r"((uint32_t)(go && wide)), "r"((uint32_t)(go && !wide)));
+    if (wide) {
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %9, 0;\n\t"
+                     "@q ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                     : "l"(p), "r"((uint32_t)go));
+    } else {
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %9, 0;\n\t"
+                     "@q ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%8];\n\t"
+                     "@q ld.global.nc.L1::no_allocate.v4.b32 {%4,%5,%6,%7}, [%8+16];\n\t}"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                     : "l"(p), "r"((uint32_t)go));
+    }
 }
 
 // E8M0 byte of a block whose largest finite magnitude is amax (amax >= 0, finite).
@@ -76,6 +83,21 @@ __device__ __forceinline__ float finite_abs(float v)
 {
     const float a = fabsf(v);
     return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// f16x2 of two floats, in one instruction (a conversion of one float takes the slow unit).
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // Four floats -> four E4M3 bytes (v[0] in the lowest), round to nearest even, saturating at 448;

@@ -111,21 +111,16 @@ cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream
 }
 
 // ------------------------------------------------------------------ matvec
-// CTAs a row tile (a cluster's size): the one that keeps the longest CTA shortest, two CTAs an SM;
-// a CTA's start and the cluster's sum cost about two chunks.
+// CTAs a row tile (a cluster's size): as many as fit the GPU together, two CTAs an SM.  At 32 tiles and
+// 56 chunks of K, 8 / 7 / 6 / 4 CTAs a tile take 13.0 / 14.4 / 17.3 / 17.8 us (NVFP4, 5 rows); at 112
+// tiles and 16 chunks, where 2 fit, 1 / 2 / 3 / 4 take 28.9 / 22.2 / 32.1 / 25.7 us (MXFP4, 16 rows).
 int matvec_ranks(int64_t tiles, int nchunks, int sms)
 {
     int best = 1;
-    int64_t least = INT64_MAX;
-    for (int r = 1; r <= 8; ++r) {
+    for (int r = 2; r <= 8 && tiles * r <= 2 * (int64_t)sms; ++r) {
         const int per = (nchunks + r - 1) / r;
-        if ((nchunks + per - 1) / per != r)
-            continue;  // some CTA would have nothing to do
-        const int64_t waves = (tiles * r + 2 * sms - 1) / (2 * sms), cost = waves * (per + 2);
-        if (cost < least) {
-            least = cost;
+        if ((nchunks + per - 1) / per == r)  // no CTA has nothing to do
             best = r;
-        }
     }
     return best;
 }
@@ -139,13 +134,13 @@ int launch_matvec(const MatvecShape &a, int tiles, int ranks, int slot, cudaStre
     if (cudaGetDevice(&dev) != cudaSuccess)
         return FP4LIN_ERR_CUDA;
     auto *kern = matvec_kernel<NV, X8, HAD, NT>;
-    const int st = raise_smem(kern, &g_matvec_attr[dev][slot], mv_smem(MV_MAX_M, MV_SEG));
+    const int st = raise_smem(kern, &g_matvec_attr[dev][slot], mv_smem(MV_MAX_M, MV_SEG, 1) + 1024);
     if (st != FP4LIN_OK)
         return st;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * ranks));
     cfg.blockDim = dim3(MV_THREADS);
-    cfg.dynamicSmemBytes = mv_smem(a.M, std::min(a.per_cta, MV_SEG));
+    cfg.dynamicSmemBytes = mv_smem(a.M, std::min(a.per_cta, MV_SEG), ranks);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -204,6 +199,7 @@ int matvec_entry(bool nv, const void *x, const uint8_t *xs, int64_t M, int64_t K
     a.nchunks = (int)((K + MV_CHUNK - 1) / MV_CHUNK);
     const int tiles = (int)((N + MV_ROWS - 1) / MV_ROWS);
     const int ranks = matvec_ranks(tiles, a.nchunks, dev->sms);
+    a.mp_shift = M > 4 ? 3 : M > 2 ? 2 : M > 1 ? 1 : 0;
     a.per_cta = (a.nchunks + ranks - 1) / ranks;
     a.wide_w = aligned(w, 32);
     cudaStream_t s = as_stream(stream);
