@@ -15,6 +15,8 @@
 // to f16 (2^-11 each, against bf16 outputs).
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "gemm_sm100.cuh"
 #include "kv_attention.cuh"  // mma_16816x
 #include "mxfp8.cuh"
@@ -32,11 +34,12 @@ struct KvPagedShape {
     const uint8_t *kc, *ks, *vc, *vs;
     const int32_t *table, *lens, *cu;
     __nv_bfloat16 *out;      // [T, H*G, D]
-    float *ws;               // [B*H, tiles, S, rows, D + 2]
+    float *ws;               // [B*H, tiles, S, rows, D + 4], where S > 1 and not joined
     int64_t ld_q, ld_t;
     float qscale;            // scale * log2(e)
     int B, H, G, T, NP, shift, max_new, max_len;
     int chunk, S, tiles;
+    bool joined;             // the S splits of a tile are one cluster
     int max_rows;            // requests of more rows are the tensor-core kernel's (kv_paged_prefill.cuh)
 };
 
@@ -117,13 +120,14 @@ __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, u
 // byte permutes of two rows' words; it takes D/8 contiguous dimensions (those of all D/16 M tiles).
 // The weights change from the score layout to B fragments by an 8 x 8 transpose in registers.
 template <int D, int NT>
-__global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShape a)
+__global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_kernel(KvPagedShape a)
 {
     constexpr int R = 8 * NT, KW = D / 16, VW = D / 32;  // rows, 32-bit words a lane needs of a K / V row
     __shared__ int s_page[KVP_MAX_CHUNK / 16];
     __shared__ float s_kf[KVP_MAX_CHUNK / 16], s_xv[KVP_MAX_CHUNK / 16];
     __shared__ float s_m[KVP_WARPS][R], s_den[KVP_WARPS][R];
     __shared__ float s_o[KVP_WARPS][R][D + 4];
+    __shared__ float s_cm[R], s_cden[R];  // of the whole CTA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
     pdl_wait();
@@ -135,20 +139,18 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
         return;
     const int imin = row0 / a.G, imax = (min(row0 + R, rows) - 1) / a.G;
     const int k0 = blockIdx.x * a.chunk, kend = rq.len + imax + 1;  // keys the tile's last row sees
-    if (k0 >= kend)
+    if (k0 >= kend && !a.joined)
         return;
     const int k1 = min(kend, k0 + a.chunk);  // rows behind len + n hold anything, and are not read
     const int P1 = (1 << a.shift) - 1;
 
-    for (int i = tid; i < (k1 - k0 + 15) / 16; i += KVP_THREADS) {
+    const int groups = max(0, k1 - k0 + 15) / 16;  // of 16 keys, which lie in one page
+    for (int i = tid; i < groups; i += KVP_THREADS) {
         const int page = a.table[b * a.ld_t + ((k0 + 16 * i) >> a.shift)];
         const bool ok = page >= 0 && page < a.NP;
         if (!ok)
             report_error(FP4LIN_ERR_OUT_OF_RANGE);
-        const uint32_t kb = ok ? a.ks[(int64_t)page * a.H + h] : 0u, vb = ok ? a.vs[(int64_t)page * a.H + h] : 0u;
         s_page[i] = ok ? page : -1;
-        s_kf[i] = mxfp8_scale(kb);
-        s_xv[i] = ok ? (vb ? (float)((int)vb - 127) : KVP_ZERO_X) : -INFINITY;  // no page: weight 0
     }
     uint32_t qb[NT][KW][2];
     float qs[NT][2];
@@ -170,50 +172,51 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
     __syncthreads();
 
     uint32_t kr[2][2][KW], vr[2][4][VW];
-    // row `key` of this head; go becomes false where there is no page
-    auto row_ptr = [&](const uint8_t *codes, int key, bool &go) {
-        const int page = go ? s_page[(key - k0) >> 4] : -1;
+    // A group of 16 keys is in one page: its rows lie together, and in bounds even where the request
+    // ends within them (scores of keys behind it are masked, its values dropped below).
+    auto group = [&](int key, bool &go) {
+        const int page = key < k1 ? s_page[(key - k0) >> 4] : -1;
         go = page >= 0;
-        return codes + (((int64_t)page * a.H + h) << a.shift) * D + (int64_t)(key & P1) * D;
+        return ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D;
     };
     auto load_k = [&](int kb) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            bool go;
+            const uint8_t *p = a.kc + group(kb + 16 * u, go) + g * D + t * (D / 4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = kb + 16 * u + 8 * e + g;
-                bool go = key < k1;
-                const uint8_t *p = row_ptr(a.kc, key, go);
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int w = 0; w < KW; w += 4) {
-                    const uint4 x = ld_nc_v4_if(p + t * (D / 4) + 4 * w, go);
+                    const uint4 x = ld_nc_v4_if(p + 8 * e * D + 4 * w, go);
                     kr[u][e][w] = x.x;
                     kr[u][e][w + 1] = x.y;
                     kr[u][e][w + 2] = x.z;
                     kr[u][e][w + 3] = x.w;
                 }
-            }
+        }
     };
     auto load_v = [&](int kb) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            bool go;
+            const uint8_t *p = a.vc + group(kb + 16 * u, go) + 2 * t * D + g * (D / 8);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int key = kb + 16 * u + 2 * t + (e & 1) + 8 * (e >> 1);
-                bool go = key < k1;
-                const uint8_t *p = row_ptr(a.vc, key, go);
+                const int row = (e & 1) + 8 * (e >> 1);
                 if constexpr (VW == 4) {
-                    const uint4 x = ld_nc_v4_if(p + g * 16, go);
+                    const uint4 x = ld_nc_v4_if(p + row * D, go);
                     vr[u][e][0] = x.x;
                     vr[u][e][1] = x.y;
                     vr[u][e][2] = x.z;
                     vr[u][e][3] = x.w;
                 } else {
-                    const uint2 x = ld_nc_v2_if(p + g * 8, go);
+                    const uint2 x = ld_nc_v2_if(p + row * D, go);
                     vr[u][e][0] = x.x;
                     vr[u][e][1] = x.y;
                 }
             }
+        }
     };
 
     float o[NT][D / 16][4], den[NT][2], M[NT][2];
@@ -225,9 +228,18 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
         for (int u = 0; u < D / 16; ++u)
             o[nt][u][0] = o[nt][u][1] = o[nt][u][2] = o[nt][u][3] = 0.0f;
     }
+    bool nan = false;
     int kb = k0 + warp * KVP_STEP;
     load_k(kb);
     load_v(kb);
+    for (int i = tid; i < groups; i += KVP_THREADS) {  // the scales, while the first rows are on their way
+        const int page = s_page[i];
+        const bool ok = page >= 0;
+        const uint32_t kbyte = ok ? a.ks[(int64_t)page * a.H + h] : 0u, vbyte = ok ? a.vs[(int64_t)page * a.H + h] : 0u;
+        s_kf[i] = mxfp8_scale(kbyte);
+        s_xv[i] = ok ? (vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X) : -INFINITY;  // no page: weight 0
+    }
+    __syncthreads();
     for (; kb < k1; kb += KVP_WARPS * KVP_STEP) {
         const bool more = kb + KVP_WARPS * KVP_STEP < k1;
         float s[2][NT][4];
@@ -311,6 +323,23 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
                 wb[u][nt][1] = movmatrix(cvt_f16x2(s[u][nt][2], s[u][nt][3]));
             }
         }
+        if (kb + KVP_STEP - 1 > rq.len + imin) {
+            // a weight of 0 must stay 0: rows behind the end hold anything, and a NaN code among the keys
+            // that not every row sees is dropped here and put in where it is seen at the end
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = kb + 16 * u + 2 * t + (e & 1) + 8 * (e >> 1);
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) {
+                        if (key >= k1)
+                            vr[u][e][w] = 0u;
+                        else if (key > rq.len + imin)
+                            nan |= drop_nan_codes(vr[u][e][w]);
+                    }
+                }
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -347,9 +376,17 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
             for (int u = 0; u < D / 16; ++u)
                 *reinterpret_cast<float2 *>(&s_o[warp][r][g * (D / 8) + 2 * u]) = make_float2(o[nt][u][e], o[nt][u][e + 2]);
         }
-    __syncthreads();
+    const bool any_nan = __syncthreads_or(nan);
     const int live_rows = min(R, rows - row0);
     const int64_t part = ((int64_t)bh * a.tiles + blockIdx.z) * a.S + blockIdx.x;
+    auto write_out = [&](int r, int d, float sum, const float *v) {
+        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum == 0.0f ? 0.0f : sum;
+        const int rho = row0 + r, tok = rho / a.G, j = rho - tok * a.G;
+        uint2 y;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(v[1] * inv), "f"(v[0] * inv));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(v[3] * inv), "f"(v[2] * inv));
+        *reinterpret_cast<uint2 *>(a.out + ((int64_t)(rq.first + tok) * a.H * a.G + h * a.G + j) * D + d) = y;
+    };
     for (int i = tid; i < live_rows * (D / 4); i += KVP_THREADS) {
         const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
         float m = s_m[0][r];
@@ -366,13 +403,24 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
             for (int j = 0; j < 4; ++j)
                 v[j] = fmaf(f, s_o[w][r][d + j], v[j]);
         }
+        if (any_nan) {
+            const int last = min(k1 - 1, rq.len + (row0 + r) / a.G);
+            for (int key = max(k0, rq.len + imin + 1); key <= last; ++key) {
+                const int page = s_page[(key - k0) >> 4];
+                const uint8_t *p = a.vc + ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D + d;
+                for (int j = 0; page >= 0 && j < 4; ++j)
+                    if ((p[j] & 127) == 127)
+                        v[j] = __int_as_float(0x7fc00000);
+            }
+        }
         if (a.S == 1) {
-            const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-            const int rho = row0 + r, tok = rho / a.G, j = rho - tok * a.G;
-            uint2 y;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.x) : "f"(v[1] * inv), "f"(v[0] * inv));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y.y) : "f"(v[3] * inv), "f"(v[2] * inv));
-            *reinterpret_cast<uint2 *>(a.out + ((int64_t)(rq.first + tok) * a.H * a.G + h * a.G + j) * D + d) = y;
+            write_out(r, d, sum, v);
+        } else if (a.joined) {
+            *reinterpret_cast<float4 *>(&s_o[0][r][d]) = make_float4(v[0], v[1], v[2], v[3]);  // read by this thread alone
+            if (d == 0) {
+                s_cm[r] = m;
+                s_cden[r] = sum;
+            }
         } else {
             float *dst = a.ws + (part * R + r) * (D + 4);
             *reinterpret_cast<float4 *>(dst + d) = make_float4(v[0], v[1], v[2], v[3]);
@@ -380,6 +428,41 @@ __global__ void __launch_bounds__(KVP_THREADS) kv_paged_split_kernel(KvPagedShap
                 *reinterpret_cast<float2 *>(dst + D) = make_float2(m, sum);
         }
     }
+    if (!a.joined)
+        return;
+    // the splits of the cluster, each CTA a share of the outputs
+    cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+    cl.sync();
+    for (int i = tid * a.S + (int)blockIdx.x; i < live_rows * (D / 4); i += KVP_THREADS * a.S) {
+        const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+        float m[8], den[8], v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float4 o4[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int from = q < a.S ? q : 0;
+            m[q] = q < a.S ? *cl.map_shared_rank(&s_cm[r], from) : -INFINITY;
+            den[q] = *cl.map_shared_rank(&s_cden[r], from);
+            o4[q] = *reinterpret_cast<const float4 *>(cl.map_shared_rank(&s_o[0][r][d], from));
+        }
+        float top = m[0], sum = 0.0f;
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+            top = fmaxf(top, m[q]);
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q < a.S) {
+                const float f = ex2(m[q] - base);
+                sum = fmaf(f, den[q], sum);
+                v[0] = fmaf(f, o4[q].x, v[0]);
+                v[1] = fmaf(f, o4[q].y, v[1]);
+                v[2] = fmaf(f, o4[q].z, v[2]);
+                v[3] = fmaf(f, o4[q].w, v[3]);
+            }
+        }
+        write_out(r, d, sum, v);
+    }
+    cl.sync();  // no CTA leaves while it is read
 }
 
 // Joins a row's splits: o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) den_s.  One warp a row.
@@ -427,7 +510,7 @@ __global__ void __launch_bounds__(128) kv_paged_merge_kernel(KvPagedShape a, int
             v[1] = fmaf(f, x.y, v[1]);
         }
     }
-    const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
+    const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
     uint32_t y[D / 64];
 #pragma unroll
     for (int k = 0; k < D / 64; ++k)

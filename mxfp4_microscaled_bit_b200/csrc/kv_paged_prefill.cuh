@@ -126,14 +126,6 @@ __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f)
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Bytes of w that are the E4M3 NaN code become 0; true if there was one.
-__device__ __forceinline__ bool drop_nan_codes(uint32_t &w)
-{
-    const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    w &= ~m;
-    return m != 0u;
-}
-
 // 16 codes of (row, 16-byte chunk cc of the row) as f16 into the operand layout at `base`: blocks of
 // 128 rows x 128 bytes, one for each 64 dimensions; 16-byte chunk x of row r sits at x ^ (r % 8).
 template <int D>

@@ -123,6 +123,14 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
         : "r"(w));
 }
 
+// Bytes of w that are the E4M3 NaN code become 0; true if there was one.
+__device__ __forceinline__ bool drop_nan_codes(uint32_t &w)
+{
+    const uint32_t m = __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    w &= ~m;
+    return m != 0u;
+}
+
 // Four E4M3 bytes times 2^-k, rounded once to E4M3.  The product is formed in f16: it is exact
 // from 2^-14 up, and everything below 2^-10 (half of E4M3's smallest step) becomes zero anyway.
 __device__ __forceinline__ uint32_t e4m3x4_shift(uint32_t w, uint32_t factor_f16x2)

@@ -78,9 +78,14 @@ KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D,
     int64_t chunk = (max_len * units + (int64_t)sms * 12 - 1) / ((int64_t)sms * 12);
     chunk = (chunk + 127) / 128 * 128;
     chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), KVP_MAX_CHUNK);
+    // a second launch costs more than a second step of the warps
+    const int64_t joined = (max_len + 8 * 128 - 1) / (8 * 128) * 128;
+    if (chunk < joined && joined <= 256)
+        chunk = joined;
     p.chunk = (int)chunk;
     p.S = (int)((max_len + chunk - 1) / chunk);
-    p.ws_bytes = p.S > 1 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
+    // up to 8 splits are one cluster, joined in the kernel; more leave their parts in the workspace
+    p.ws_bytes = p.S > 8 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
     return p;
 }
 
@@ -101,10 +106,21 @@ cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream
         if (e != cudaSuccess)
             return e;
     }
-    const dim3 grid((unsigned)p.S, (unsigned)(a.B * a.H), (unsigned)p.tiles);
-    cudaError_t e = p.nt == 1 ? launch_pdl(kv_paged_split_kernel<D, 1>, grid, dim3(KVP_THREADS), 0, s, a)
-                              : launch_pdl(kv_paged_split_kernel<D, 2>, grid, dim3(KVP_THREADS), 0, s, a);
-    if (e != cudaSuccess || p.S == 1)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.S, (unsigned)(a.B * a.H), (unsigned)p.tiles);
+    cfg.blockDim = dim3(KVP_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.S;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.joined ? 2 : 1;
+    const cudaError_t e = p.nt == 1 ? cudaLaunchKernelEx(&cfg, kv_paged_split_kernel<D, 1>, a)
+                                    : cudaLaunchKernelEx(&cfg, kv_paged_split_kernel<D, 2>, a);
+    if (e != cudaSuccess || p.S <= 8)
         return e;
     const dim3 mgrid((unsigned)((std::min<int64_t>((int64_t)a.max_new * a.G, p.max_rows) + 3) / 4), (unsigned)(a.B * a.H));
     return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, p.rows);
@@ -431,6 +447,7 @@ int kv_fp8_attention(const void *q, int64_t ld_q, int T, const uint8_t *k_codes,
     a.S = p.S;
     a.tiles = p.tiles;
     a.max_rows = p.max_rows;
+    a.joined = p.S > 1 && p.S <= 8;
     if (p.prefill_tiles) {
         int ordinal = 0;
         if (cudaGetDevice(&ordinal) != cudaSuccess)

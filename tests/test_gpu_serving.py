@@ -465,6 +465,29 @@ def test_attention_extreme_magnitudes(new, q_scale, v_shift):
     status_ok()
 
 
+@pytest.mark.parametrize("G,new", [(2, 5), (4, 60), (1, 300)])
+def test_attention_nan_values_reach_only_the_rows_that_see_them(G, new):
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(2, 2, G, 64, 32, [70, 0], [new, new], seed=11)
+    for b, p, h, d in ((0, 70 + new // 2, 1, 9), (0, 71, 0, 63), (1, new - 1, 1, 0)):
+        vc[table[b, p // 32], h, p % 32, d] = 0xFF if d else 0x7F
+    out = torch.zeros(q.shape, dtype=torch.bfloat16, device=DEV)
+    fl.kv_fp8_attention(q.to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu), max_new=new,
+                        max_len=70 + new, out=out)
+    status_ok()
+    got, want = ref.f64(out), ref.attention(ref.f64(q), kc, kb, vc, vb, table, lens, cu, 32, 0.125)[0]
+    # the reference gives every key that a row does not see no part in it
+    assert np.array_equal(np.isnan(got[:2 * new]), np.isnan(want[:2 * new]))
+    ok = ~np.isnan(want)
+    assert np.abs(got[ok] - want[ok]).max() < 0.05
+
+
+@pytest.mark.parametrize("L", [100, 129, 900, 1024, 1100, 2048, 2300, 20000])
+def test_attention_split_counts(L):
+    """One split, the cluster's two to eight, and the workspace's many."""
+    attention_check(*attention_case(2, 1, 4, 64, 32, [L - 1, L // 3], [1, 1], seed=L), 32)
+    status_ok()
+
+
 def test_attention_skips_and_reports_what_breaks_its_bounds():
     q, caches, table, lens, cu = attention_case(3, 1, 2, 64, 16, [20, 40, 3], [2, 3, 1], seed=2)
     (kc, kb), (vc, vb) = caches
@@ -504,18 +527,18 @@ def test_attention_skips_and_reports_what_breaks_its_bounds():
 
 
 def test_attention_refusals():
-    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(1, 2, 2, 64, 16, [700], [1])
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(1, 2, 2, 64, 16, [3000], [1])
     a = [q.to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu)]
     with pytest.raises(fl.Fp4LinError, match="INVALID"):
         fl.kv_fp8_attention(*a, max_new=1, max_len=table.shape[1] * 16 + 1)
     with pytest.raises(fl.Fp4LinError, match="WORKSPACE"):
-        fl.kv_fp8_attention(*a, max_new=1, max_len=701, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+        fl.kv_fp8_attention(*a, max_new=1, max_len=3001, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="a multiple of 2 heads"):
-        fl.kv_fp8_attention(a[0][:, :3], *a[1:], max_new=1, max_len=701)
+        fl.kv_fp8_attention(a[0][:, :3], *a[1:], max_new=1, max_len=3001)
     with pytest.raises(TypeError, match="pair"):
-        fl.kv_fp8_attention(a[0], a[1][0][0], *a[2:], max_new=1, max_len=701)
+        fl.kv_fp8_attention(a[0], a[1][0][0], *a[2:], max_new=1, max_len=3001)
     with pytest.raises(TypeError, match="lens must be torch.int32"):
-        fl.kv_fp8_attention(*a[:4], a[4].long(), a[5], max_new=1, max_len=701)
+        fl.kv_fp8_attention(*a[:4], a[4].long(), a[5], max_new=1, max_len=3001)
     status_ok()
 
 
