@@ -29,6 +29,12 @@ SERVING_EXPORTS = {
 
 _BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 
+try:  # torch.empty on the current CUDA device in a third of the time
+    from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided
+except ImportError:
+    def _empty_strided(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+
 
 _library = None
 
@@ -120,6 +126,14 @@ def _scale_bytes(rows: int, cols: int) -> int:
 
 
 # ------------------------------------------------------------------ norm
+def _apart(fn, s, ld_s, others, rows, cols):
+    """summed [rows, cols] at s is another's memory, or shares none with it."""
+    for name, lo, ld in others:
+        if s < lo + ((rows - 1) * ld + cols) * 2 and lo < s + ((rows - 1) * ld_s + cols) * 2:
+            if s != lo or (ld_s != ld and rows > 1):
+                raise ValueError(f"{fn}: summed overlaps {name} without being it")
+
+
 def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, *, eps: float = 1e-6,
                   hadamard: int = 0, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                   summed: torch.Tensor | None = None, stream=None):
@@ -142,25 +156,22 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         ld_r = _rows(fn, "residual", residual, _BF16, (rows, cols), cols, dev)
         r = residual.data_ptr()
         if summed is None:
-            summed = x.new_empty((rows, cols))
+            summed = _empty_strided((rows, cols), (cols, 1), _BF16)
             made.append(summed)
         else:
             ld_s = _rows(fn, "summed", summed, _BF16, (rows, cols), cols, dev)
+            _apart(fn, summed.data_ptr(), ld_s, (("residual", r, ld_r), ("x", x.data_ptr(), ld_x)), rows, cols)
         s = summed.data_ptr()
-        for name, t, ld in (("residual", residual, ld_r), ("x", x, ld_x)):
-            lo, hi = t.data_ptr(), t.data_ptr() + ((rows - 1) * ld + cols) * 2
-            if s < hi and lo < s + ((rows - 1) * ld_s + cols) * 2 and (s != lo or (ld_s != ld and rows > 1)):
-                raise ValueError(f"{fn}: summed overlaps {name} without being it")
     elif summed is not None:
         raise ValueError(f"{fn}: summed is the sum with a residual, and there is none")
     if codes is None:
-        codes = x.new_empty((rows, cols), dtype=_U8)
+        codes = _empty_strided((rows, cols), (cols, 1), _U8)
         made.append(codes)
     else:
         _arg(fn, "codes", codes, _U8, rows * cols, dev)
     need = _scale_bytes(rows, cols // 32)
     if scales is None:
-        scales = x.new_empty(need, dtype=_U8)
+        scales = _empty_strided((need,), (1,), _U8)
         made.append(scales)
     else:
         _arg(fn, "scales", scales, _U8, need, dev)
@@ -191,7 +202,7 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
     ldy = N
     made = out is None
     if made:
-        out = x.new_empty((M, N), dtype=_BF16)
+        out = _empty_strided((M, N), (N, 1), _BF16)
     else:
         ldy = _rows(fn, "out", out, _BF16, (M, N), N, dev)
     if nv:
@@ -252,17 +263,17 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
     if max_tokens < 1:
         raise ValueError(f"{fn}: max_tokens must be at least 1, not {max_tokens}")
     if cu_new is None:
-        cu_new = block_table.new_empty(B + 1)
+        cu_new = _empty_strided((B + 1,), (1,), _I32)
         made.append(cu_new)
     else:
         _arg(fn, "cu_new", cu_new, _I32, B + 1, dev)
     if slots is None:
-        slots = block_table.new_empty(max_tokens)
+        slots = _empty_strided((max_tokens,), (1,), _I32)
         made.append(slots)
     else:
         _arg(fn, "slots", slots, _I32, max_tokens, dev)
     if next_head is None:
-        next_head = block_table.new_empty(1)
+        next_head = _empty_strided((1,), (1,), _I32)
         made.append(next_head)
     else:
         _arg(fn, "next_head", next_head, _I32, 1, dev)
@@ -338,7 +349,7 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
     pcu = _arg(fn, "cu_new", cu_new, _I32, B + 1, dev)
     made = []
     if out is None:
-        out = q.new_empty((T, HQ, D))
+        out = _empty_strided((T, HQ, D), (HQ * D, D, 1), _BF16)
         made.append(out)
     else:
         _arg(fn, "out", out, _BF16, T * HQ * D, dev)
@@ -347,7 +358,7 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
         need = L.kv_fp8_attention_workspace_bytes(B, H, G, max_new, max_len, D)
         pw = None
         if need:
-            workspace = q.new_empty(need, dtype=_U8)
+            workspace = _empty_strided((need,), (1,), _U8)
             made.append(workspace)
             pw = workspace.data_ptr()
     else:
