@@ -159,12 +159,14 @@ __global__ void __launch_bounds__(TABLE_THREADS) kv_table_kernel(TableShape a)
 // finds the page's older rows under its old scale: the larger of the two exponents is the page's
 // new one, and when it grew the older rows are re-encoded to it.
 //   2 (in) + 1 (out) bytes a value, for K and V; HBM bound for prompts, latency bound for single
-// tokens.  A CTA owns the runs that begin in its `per_cta` tokens, for one head of K or of V.
-// With few runs its warps share each run's rows (the values stay in registers between the
-// maximum and the encoding); with many, as in decoding, each warp takes a run.
+// tokens.  A CTA owns the runs that begin in its `per_cta` tokens, for one head of K or of V; the
+// CTAs of a token's heads are neighbours, so that its row is read together.  A warp takes up to 16
+// rows, all loads in flight and the values in registers between the maximum and the encoding;
+// P/16 warps are a group that takes a run.  With many runs, as in decoding, each warp takes a run
+// for itself, row by row.
 constexpr int APPEND_THREADS = 256;
 constexpr int APPEND_WARPS = APPEND_THREADS / 32;
-constexpr int APPEND_TOKENS = 32;  // most tokens a CTA looks at
+constexpr int APPEND_TOKENS = 128;  // most tokens a CTA looks at
 
 struct AppendShape {
     const __nv_bfloat16 *k, *v;  // [T, H, D], token strides ld_k, ld_v
@@ -174,7 +176,7 @@ struct AppendShape {
     int T, H, shift, per_cta;
 };
 
-// Rows of `from .. to` step `step` of a run: largest finite magnitude.
+// Largest finite magnitude of eight bf16.
 __device__ __forceinline__ float bf16x8_amax(uint4 u)
 {
     float f[8], m = 0.0f;
@@ -202,40 +204,55 @@ __device__ __forceinline__ uint32_t f16x2_pow2_neg(int k)
     return h | (h << 16);
 }
 
-template <int D>
-__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(AppendShape a)
+// The warps of a group meet (named barrier 1 + group).
+__device__ __forceinline__ void append_meet(int group, int warps)
 {
-    constexpr int LPR = D / 8;       // lanes a row (8 values each)
-    constexpr int RPW = 32 / LPR;    // rows a warp pass
-    constexpr int RPC = RPW * APPEND_WARPS;
-    constexpr int PASSES = 128 / RPC;  // pages have at most 128 rows
+    if (warps == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(APPEND_THREADS, 3) kv_append_kernel(AppendShape a)
+{
+    constexpr int LPR = D / 8;         // lanes a row (8 values each)
+    constexpr int RPW = 32 / LPR;      // rows a warp pass
+    constexpr int PASSES = 16 / RPW;   // of a warp's 16 rows
     __shared__ int s_t[APPEND_TOKENS], s_slot[APPEND_TOKENS], s_n[APPEND_TOKENS], s_runs;
     __shared__ float s_max[APPEND_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int P = 1 << a.shift, h = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
+    const int P = 1 << a.shift, h = blockIdx.x >> 1;
+    const bool is_v = blockIdx.x & 1;
     const __nv_bfloat16 *x = (is_v ? a.v : a.k) + (int64_t)h * D;
     const int64_t ld = is_v ? a.ld_v : a.ld_k;
     uint8_t *codes = is_v ? a.vc : a.kc, *scales = is_v ? a.vs : a.ks;
     pdl_wait();
-    const int t0 = blockIdx.x * a.per_cta;
     if (warp == 0) {  // the runs that begin here
-        const int t = t0 + lane;
-        const bool mine = lane < a.per_cta && t < a.T;
-        const int slot = mine ? a.slots[t] : -1;
-        const int prev = mine && t > 0 ? a.slots[t - 1] : -2;
-        const bool range = slot >= 0 && slot < a.slots_end;
-        if (mine && slot != -1 && !range)
-            report_error(FP4LIN_ERR_OUT_OF_RANGE);
-        const bool lead = range && ((slot & (P - 1)) == 0 || prev != slot - 1);
-        const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-        if (lead) {
-            const int i = __popc(leads & ((1u << lane) - 1u));
-            s_t[i] = t;
-            s_slot[i] = slot;
+        const int t0 = blockIdx.y * a.per_cta, t1 = min(t0 + a.per_cta, a.T);
+        int slot[APPEND_TOKENS / 32], prev[APPEND_TOKENS / 32], runs = 0;
+#pragma unroll
+        for (int k = 0; k < APPEND_TOKENS / 32; ++k) {
+            const int t = t0 + 32 * k + lane;
+            slot[k] = t < t1 ? a.slots[t] : -1;
+            prev[k] = t < t1 && t > 0 ? a.slots[t - 1] : -2;
+        }
+#pragma unroll
+        for (int k = 0; k < APPEND_TOKENS / 32; ++k) {
+            const bool range = slot[k] >= 0 && slot[k] < a.slots_end;
+            if (slot[k] != -1 && !range)
+                report_error(FP4LIN_ERR_OUT_OF_RANGE);
+            const bool lead = range && ((slot[k] & (P - 1)) == 0 || prev[k] != slot[k] - 1);
+            const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+            if (lead) {
+                const int i = runs + __popc(leads & ((1u << lane) - 1u));
+                s_t[i] = t0 + 32 * k + lane;
+                s_slot[i] = slot[k];
+            }
+            runs += __popc(leads);
         }
         if (lane == 0)
-            s_runs = __popc(leads);
+            s_runs = runs;
     }
     __syncthreads();
     const int runs = s_runs;
@@ -258,62 +275,52 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(AppendShape a
     __syncthreads();
     const int sub = lane / LPR, col = (lane % LPR) * 8;
     const bool by_warp = runs >= APPEND_WARPS;
-    for (int i = by_warp ? warp : 0; i < runs; i += by_warp ? APPEND_WARPS : 1) {
+    const int warps = by_warp ? 1 : P / 16, group = warp / warps, in_group = warp - group * warps;
+    for (int i = group; i < runs; i += APPEND_WARPS / warps) {
         const int t = s_t[i], slot = s_slot[i], n = s_n[i], off = slot & (P - 1);
         const int64_t page_head = (int64_t)(slot >> a.shift) * a.H + h;
-        uint8_t *dst = codes + page_head * P * D;
+        uint8_t *dst = codes + page_head * P * D + col;
         const __nv_bfloat16 *src = x + (int64_t)t * ld + col;
-        uint32_t old = off ? scales[page_head] : 0u;
-        const int first = by_warp ? sub : warp * RPW + sub, step = by_warp ? RPW : RPC;
-        uint4 held[PASSES];
+        const uint32_t old = off ? scales[page_head] : 0u;
+        const int first = 16 * in_group + sub, step = 16 * warps;
+        uint4 held[PASSES];  // the warp's first 16 rows
         float m = 0.0f;
-        if (!by_warp) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p)
-                if (first + p * RPC < n) {
-                    held[p] = ld_nc_v4(src + (int64_t)(first + p * RPC) * ld);
-                    m = fmaxf(m, bf16x8_amax(held[p]));
-                }
-        } else {
-            for (int r = first; r < n; r += step)
+        for (int p = 0; p < PASSES; ++p)
+            held[p] = ld_nc_v4_if(src + (int64_t)(first + p * RPW) * ld, first + p * RPW < n);
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p)
+            m = fmaxf(m, bf16x8_amax(held[p]));
+        for (int r0 = first + step; r0 < n; r0 += step)  // a warp alone with a longer run
+            for (int r = r0; r < min(r0 + 16, n); r += RPW)
                 m = fmaxf(m, bf16x8_amax(ld_nc_v4(src + (int64_t)r * ld)));
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!by_warp) {
+        m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // in order, as none is negative
+        if (warps > 1) {
             if (lane == 0)
                 s_max[warp] = m;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < APPEND_WARPS; ++w)
-                m = fmaxf(m, s_max[w]);
+            append_meet(group, warps);
+            for (int w = 0; w < warps; ++w)
+                m = fmaxf(m, s_max[group * warps + w]);
         }
         const uint32_t byte = max(mxfp8_scale_byte(m), old);
         const float inv = mxfp8_inverse(byte);
-        if (!by_warp) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p)
-                if (first + p * RPC < n)
-                    *reinterpret_cast<uint2 *>(dst + (off + first + p * RPC) * D + col) = bf16x8_encode(held[p], inv);
-        } else {
-            for (int r = first; r < n; r += step)
-                *reinterpret_cast<uint2 *>(dst + (off + r) * D + col) =
-                    bf16x8_encode(ld_nc_v4(src + (int64_t)r * ld), inv);
-        }
+        for (int p = 0; p < PASSES; ++p)
+            if (first + p * RPW < n)
+                *reinterpret_cast<uint2 *>(dst + (off + first + p * RPW) * D) = bf16x8_encode(held[p], inv);
+        for (int r0 = first + step; r0 < n; r0 += step)
+            for (int r = r0; r < min(r0 + 16, n); r += RPW)
+                *reinterpret_cast<uint2 *>(dst + (off + r) * D) = bf16x8_encode(ld_nc_v4(src + (int64_t)r * ld), inv);
         if (off && byte > old && old) {  // older rows (all zero codes under byte 0) to the larger exponent
             const uint32_t f = f16x2_pow2_neg((int)(byte - old));
-            for (int r = first; r < off; r += step) {
-                uint2 *c = reinterpret_cast<uint2 *>(dst + r * D + col);
+            for (int r = in_group * RPW + sub; r < off; r += warps * RPW) {
+                uint2 *c = reinterpret_cast<uint2 *>(dst + r * D);
                 const uint2 v = *c;
                 *c = make_uint2(e4m3x4_shift(v.x, f), e4m3x4_shift(v.y, f));
             }
         }
-        if (!by_warp)
-            __syncthreads();  // every thread has read the old scale and s_max
-        else
-            __syncwarp();
-        if (by_warp ? lane == 0 : tid == 0)
+        append_meet(group, warps);  // every warp has read the old scale and s_max
+        if (in_group == 0 && lane == 0)
             scales[page_head] = (uint8_t)byte;
     }
 }

@@ -63,99 +63,113 @@ __device__ __forceinline__ void st_32B(void *p, bool wide, const uint32_t *v)
 }
 
 // THREADS 128: each of the CTA's four warps has a row of its own (cols <= 1024); else the CTA, of
-// cols/32 threads rounded up to whole warps and at most THREADS, has one row.
+// cols/32 threads rounded up to whole warps and at most THREADS, has one row.  The grid walks the
+// rows: the weights stay in registers, and the next row is on its way while this one is reduced.
 template <int HAD, int THREADS>
 __global__ void __launch_bounds__(THREADS) rmsnorm_mxfp8_kernel(NormShape a)
 {
     constexpr bool WARP_ROWS = THREADS == 128;
-    __shared__ float s_part[32];
+    constexpr int RPC = WARP_ROWS ? 4 : 1;  // rows a CTA
+    constexpr bool AHEAD = THREADS <= 512;  // else there are no registers for a second row
+    __shared__ float s_part[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = WARP_ROWS ? (int64_t)blockIdx.x * 4 + warp : (int64_t)blockIdx.x;
     const int blk = WARP_ROWS ? lane : (int)threadIdx.x, nblk = a.cols / 32;
-    pdl_wait();
-    if (row >= a.rows_pad)
-        return;  // whole warps only
-    const int64_t word = tc_offset(row, blk, a.katoms) & ~(int64_t)3;
-    if (row >= a.rows) {  // padding rows of the scale layout
-        if ((blk & 3) == 0 && blk < 4 * a.katoms)
-            *reinterpret_cast<uint32_t *>(a.scales + word) = 0u;
-        return;
-    }
     const bool live = blk < nblk;
-    uint32_t wr[16];
-    float v[32];
-    if (live) {
-        uint32_t xr[16];
-        load_bf16x32(a.x + row * a.ld_x + blk * 32, a.wide_x, xr);
-        if (a.r) {
-            uint32_t rr[16];
-            load_bf16x32(a.r + row * a.ld_r + blk * 32, a.wide_r, rr);
+    const int64_t step = (int64_t)gridDim.x * RPC;
+    int64_t row = (int64_t)blockIdx.x * RPC + (WARP_ROWS ? warp : 0);
+    uint32_t wr[16], xr[16], rr[16];
+    auto load = [&](int64_t at) {
+        if (live && at < a.rows) {
+            load_bf16x32(a.x + at * a.ld_x + blk * 32, a.wide_x, xr);
+            if (a.r)
+                load_bf16x32(a.r + at * a.ld_r + blk * 32, a.wide_r, rr);
+        }
+    };
+    pdl_wait();
+    if (AHEAD)
+        load(row);
+    if (live)
+        load_bf16x32(a.w + blk * 32, a.wide_w, wr);
+    for (int turn = 0; row < a.rows_pad; row += step, turn ^= 1) {  // the same rows for a whole warp (CTA)
+        const int64_t word = tc_offset(row, blk, a.katoms) & ~(int64_t)3;
+        if (row >= a.rows) {  // padding rows of the scale layout
+            if ((blk & 3) == 0 && blk < 4 * a.katoms)
+                *reinterpret_cast<uint32_t *>(a.scales + word) = 0u;
+            continue;
+        }
+        if (!AHEAD)
+            load(row);
+        float v[32], sum = 0.0f;
+        if (live) {
+            if (a.r) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float lo = __fadd_rn(__uint_as_float(xr[i] << 16), __uint_as_float(rr[i] << 16));
+                    const float hi = __fadd_rn(__uint_as_float(xr[i] & 0xFFFF0000u), __uint_as_float(rr[i] & 0xFFFF0000u));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(xr[i]) : "f"(hi), "f"(lo));
+                }
+                st_32B(a.s + row * a.ld_s + blk * 32, a.wide_s, xr);
+                st_32B(a.s + row * a.ld_s + blk * 32 + 16, a.wide_s, xr + 8);
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const float lo = __fadd_rn(__uint_as_float(xr[i] << 16), __uint_as_float(rr[i] << 16));
-                const float hi = __fadd_rn(__uint_as_float(xr[i] & 0xFFFF0000u), __uint_as_float(rr[i] & 0xFFFF0000u));
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(xr[i]) : "f"(hi), "f"(lo));
+                v[2 * i] = __uint_as_float(xr[i] << 16);
+                v[2 * i + 1] = __uint_as_float(xr[i] & 0xFFFF0000u);
             }
-            st_32B(a.s + row * a.ld_s + blk * 32, a.wide_s, xr);
-            st_32B(a.s + row * a.ld_s + blk * 32 + 16, a.wide_s, xr + 8);
+            float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                s4[i & 3] = fmaf(v[i], v[i], s4[i & 3]);
+            sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
         }
-        load_bf16x32(a.w + blk * 32, a.wide_w, wr);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[2 * i] = __uint_as_float(xr[i] << 16);
-            v[2 * i + 1] = __uint_as_float(xr[i] & 0xFFFF0000u);
-        }
-    }
-    float sum = 0.0f;
-    if (live)
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            sum = fmaf(v[i], v[i], sum);
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!WARP_ROWS) {
-        if (lane == 0)
-            s_part[warp] = sum;
-        __syncthreads();
-        const int warps = (int)blockDim.x >> 5;
-        sum = lane < warps ? s_part[lane] : 0.0f;
+        if (AHEAD)
+            load(row + step);
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    const float rs = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
-    uint32_t byte = 0u;
-    if (live) {
+        if (!WARP_ROWS) {
+            if (lane == 0)
+                s_part[turn][warp] = sum;
+            __syncthreads();
+            const int warps = (int)blockDim.x >> 5;
+            sum = lane < warps ? s_part[turn][lane] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[2 * i] = __fmul_rn(__fmul_rn(v[2 * i], rs), __uint_as_float(wr[i] << 16));
-            v[2 * i + 1] = __fmul_rn(__fmul_rn(v[2 * i + 1], rs), __uint_as_float(wr[i] & 0xFFFF0000u));
+            for (int o = 16; o; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        if constexpr (HAD == 16) {
-            fwht_scaled_packed<16>(v, 0.25f);
-            fwht_scaled_packed<16>(v + 16, 0.25f);
-        } else if constexpr (HAD == 32) {
-            fwht_scaled_packed<32>(v, __uint_as_float(0x3E3504F3u));
+        const float rs = __frsqrt_rn(fmaf(sum, a.inv_cols, a.eps));
+        uint32_t byte = 0u;
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[2 * i] = __fmul_rn(__fmul_rn(v[2 * i], rs), __uint_as_float(wr[i] << 16));
+                v[2 * i + 1] = __fmul_rn(__fmul_rn(v[2 * i + 1], rs), __uint_as_float(wr[i] & 0xFFFF0000u));
+            }
+            if constexpr (HAD == 16) {
+                fwht_scaled_packed<16>(v, 0.25f);
+                fwht_scaled_packed<16>(v + 16, 0.25f);
+            } else if constexpr (HAD == 32) {
+                fwht_scaled_packed<32>(v, __uint_as_float(0x3E3504F3u));
+            }
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                amax = fmaxf(amax, finite_abs(v[i]));
+            byte = mxfp8_scale_byte(amax);
+            const float inv = mxfp8_inverse(byte);
+            uint32_t c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+            st_32B(a.codes + row * a.cols + blk * 32, a.wide_c, c);
         }
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            amax = fmaxf(amax, finite_abs(v[i]));
-        byte = mxfp8_scale_byte(amax);
-        const float inv = mxfp8_inverse(byte);
-        uint32_t c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            c[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-        st_32B(a.codes + row * a.cols + blk * 32, a.wide_c, c);
+        // four lanes' bytes make one word of the scale layout (zero in padding columns)
+        uint32_t sw = byte << (8 * (lane & 3));
+        sw |= __shfl_xor_sync(0xffffffffu, sw, 1);
+        sw |= __shfl_xor_sync(0xffffffffu, sw, 2);
+        if ((lane & 3) == 0 && blk < 4 * a.katoms)
+            *reinterpret_cast<uint32_t *>(a.scales + word) = sw;
     }
-    // four lanes' bytes make one word of the scale layout (zero in padding columns)
-    uint32_t sw = byte << (8 * (lane & 3));
-    sw |= __shfl_xor_sync(0xffffffffu, sw, 1);
-    sw |= __shfl_xor_sync(0xffffffffu, sw, 2);
-    if ((lane & 3) == 0 && blk < 4 * a.katoms)
-        *reinterpret_cast<uint32_t *>(a.scales + word) = sw;
 }
 
 }  // namespace fp4lin

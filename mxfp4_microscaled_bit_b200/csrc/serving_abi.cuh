@@ -42,15 +42,23 @@ inline int launched(cudaError_t e)
 }
 
 // ------------------------------------------------------------------ norm
+// As many CTAs as are resident together at 128 registers a thread; they walk the rows.  8192 x 4096
+// with 4 / 8 / 12 / 16 / all CTAs of 128 threads an SM: 39.2 / 39.9 / 40.9 / 40.9 / 47 us.
+unsigned norm_grid(int64_t ctas, int threads, int sms)
+{
+    return (unsigned)std::min<int64_t>(ctas, (int64_t)sms * std::max(1, 512 / threads));
+}
+
 template <int HAD>
-cudaError_t launch_norm(const NormShape &a, cudaStream_t s)
+cudaError_t launch_norm(const NormShape &a, int sms, cudaStream_t s)
 {
     const int lanes = (a.cols / 32 + 31) / 32 * 32;
     if (lanes == 32)
-        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 128>, dim3((unsigned)((a.rows_pad + 3) / 4)), dim3(128), 0, s, a);
+        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 128>, dim3(norm_grid((a.rows_pad + 3) / 4, 128, sms)), dim3(128), 0, s, a);
+    const dim3 grid(norm_grid(a.rows_pad, lanes, sms));
     if (lanes <= 512)
-        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 512>, dim3((unsigned)a.rows_pad), dim3(lanes), 0, s, a);
-    return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 1024>, dim3((unsigned)a.rows_pad), dim3(lanes), 0, s, a);
+        return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 512>, grid, dim3(lanes), 0, s, a);
+    return launch_pdl(rmsnorm_mxfp8_kernel<HAD, 1024>, grid, dim3(lanes), 0, s, a);
 }
 
 // ------------------------------------------------------------------ attention
@@ -275,9 +283,9 @@ int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_
     a.wide_w = aligned(weight, 32);
     a.wide_c = aligned(codes, 32);
     cudaStream_t s = as_stream(stream);
-    return launched(hadamard == 16   ? launch_norm<16>(a, s)
-                    : hadamard == 32 ? launch_norm<32>(a, s)
-                                     : launch_norm<0>(a, s));
+    return launched(hadamard == 16   ? launch_norm<16>(a, dev->sms, s)
+                    : hadamard == 32 ? launch_norm<32>(a, dev->sms, s)
+                                     : launch_norm<0>(a, dev->sms, s));
 }
 
 int nvfp4_matvec(const void *x, const uint8_t *x_scales, int64_t M, int64_t K, int64_t ld_x, int hadamard,
@@ -347,7 +355,7 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
     if (T < 1 || H < 1 || D < 1 || num_pages < 1 || ld_k < (int64_t)H * D || ld_v < (int64_t)H * D)
         return FP4LIN_ERR_INVALID_ARGUMENT;
     const int shift = page_shift(page);
-    if (shift < 0 || (D != 64 && D != 128) || ld_k % 8 != 0 || ld_v % 8 != 0 || H > 32767 ||
+    if (shift < 0 || (D != 64 && D != 128) || ld_k % 8 != 0 || ld_v % 8 != 0 || H > 32767 || T > 65535 * APPEND_TOKENS ||
         ((int64_t)num_pages << shift) > 0x7FFFFFFF)
         return FP4LIN_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) ||
@@ -371,11 +379,11 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
     a.T = T;
     a.H = H;
     a.shift = shift;
-    // fewer tokens a CTA while there are fewer CTAs than the SMs hold
+    // fewer tokens a CTA while there are fewer CTAs than the SMs hold, down to a token a warp
     a.per_cta = APPEND_TOKENS;
-    while (a.per_cta > 1 && (int64_t)((T + a.per_cta - 1) / a.per_cta) * H * 2 < (int64_t)dev->sms * 8)
+    while (a.per_cta > APPEND_WARPS && (int64_t)((T + a.per_cta - 1) / a.per_cta) * H * 2 < (int64_t)dev->sms * 3)
         a.per_cta /= 2;
-    const dim3 grid((unsigned)((T + a.per_cta - 1) / a.per_cta), (unsigned)(2 * H));
+    const dim3 grid((unsigned)(2 * H), (unsigned)((T + a.per_cta - 1) / a.per_cta));
     cudaStream_t s = as_stream(stream);
     return launched(D == 64 ? launch_pdl(kv_append_kernel<64>, grid, dim3(APPEND_THREADS), 0, s, a)
                             : launch_pdl(kv_append_kernel<128>, grid, dim3(APPEND_THREADS), 0, s, a));
