@@ -27,37 +27,75 @@ constexpr int KPP_SLOTS = 4;           // blocks whose page factors are held at 
 constexpr float KPP_LAZY = 8.0f;       // log2 growth of the maximum that is let pass
 
 struct KppCtrl {
-    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], odone[2], drain;
-    float kf[KPP_SLOTS][8], xv[KPP_SLOTS][8], c[KPP_SLOTS][8];
+    uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2][2], pfull[2][2], odone[2], drain;
+    alignas(16) float kf[KPP_SLOTS][8], xv[KPP_SLOTS][8], c[KPP_SLOTS][8];
     uint32_t tmem;
     int abort, nan;
 };
 
 constexpr size_t kpp_smem(int D) { return 1024 + (size_t)(KPP_ROWS + 4 * KPP_KEYS) * D * 2 + sizeof(KppCtrl); }
 
-// D[128 x N] (+)= A[128 x 16] B[N x 16]^T, f16 operands: A in shared memory, or (ts) in TMEM.
-__device__ __forceinline__ void mma_f16_ss_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// One lane of a converged warp issues a whole batch, so that little stands between the MMAs (the warp
+// shares its scheduler with a softmax's): D[128 x N] = sum over D/16 steps of A[128 x 16] B[N x 16]^T,
+// f16 operands in shared memory (descriptors of their first steps; 32 bytes a step, the next 64
+// dimensions 16 KB on).  Then `bar` hears of it, and at once of what this warp has waited for.
+template <int D>
+__device__ __forceinline__ void kpp_issue_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t *bar)
 {
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
+    if constexpr (D == 128)
+        asm volatile("{\n\t.reg .pred e, on, off;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "setp.eq.u32 on, %3, %3;\n\tsetp.ne.u32 off, %3, %3;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, off;\n\t"
+                 "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+                 "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%4];\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred e, on, off;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "setp.eq.u32 on, %3, %3;\n\tsetp.ne.u32 off, %3, %3;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, off;\n\t"
+                 "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, on;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+                 "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%4];\n\t}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
+                     : "memory");
 }
 
-__device__ __forceinline__ void mma_f16_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// The same for D[128 x N] (+)= P V over 64 keys: P in TMEM (8 columns a step), V MN-major (2 KB a step).
+__device__ __forceinline__ void kpp_issue_values(uint32_t d, uint32_t p, uint64_t v, uint32_t idesc, uint32_t acc,
+                                                 uint64_t *bar)
 {
-    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-// One arrival of a converged warp, which stays converged (a branch on the lane before the MMAs
-// makes their issue three times slower).
-__device__ __forceinline__ void mbar_arrive_w(uint64_t *bar)
-{
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
+    asm volatile("{\n\t.reg .pred e, on, first;\n\t.reg .b64 y;\n\t.reg .b32 t;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "setp.eq.u32 on, %3, %3;\n\tsetp.ne.u32 first, %5, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, first;\n\t"
+                 "add.u32 t, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], y, %3, on;\n\t"
+                 "add.u32 t, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], y, %3, on;\n\t"
+                 "add.u32 t, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], y, %3, on;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t"
+                 "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%4];\n\t}" ::"r"(d),
+                 "r"(p), "l"(v), "r"(idesc), "r"(smem_u32(bar)), "r"(acc)
                  : "memory");
 }
 
@@ -150,24 +188,6 @@ __device__ __forceinline__ void kpp_convert(uint8_t *base, int row, int cc, uint
 // the -inf of a masked score stays one.
 __device__ __forceinline__ float kpp_factor(float kf, float qs) { return fmaxf(kf * qs, 1.17549435e-38f); }
 
-// Scores of the row's columns behind `last` become -inf.
-__device__ __noinline__ void kpp_mask(uint32_t t_s, int last)
-{
-#pragma unroll 1
-    for (int k = 0; k < KPP_KEYS; k += 8) {
-        float v[8];
-        tmem_ld8(t_s + k, v);
-        uint32_t r[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            r[j] = k + j > last ? 0xFF800000u : __float_as_uint(v[j]);
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
-                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t_s + k)
-                     : "memory");
-    }
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a, int min_rows)
 {
@@ -199,8 +219,10 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             mbar_init(&ct.kfree[i], 1);
             mbar_init(&ct.vfull[i], 128);
             mbar_init(&ct.vfree[i], 1);
-            mbar_init(&ct.sfull[i], 2);
-            mbar_init(&ct.pfull[i], 128);
+            for (int half = 0; half < 2; ++half) {
+                mbar_init(&ct.sfull[i][half], 2);
+                mbar_init(&ct.pfull[i][half], 128);
+            }
             mbar_init(&ct.odone[i], 2);
         }
         mbar_init(&ct.drain, 1);
@@ -258,39 +280,47 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             const int lim = mine ? rq.len + tok : -1;
             float M = -INFINITY, den = 0.0f;
             bool ok = true;
-            for (int i = 0; i < blocks; ++i) {
-                ok = warp_wait(&ct.sfull[tile], i & 1, abort, lane);
+#pragma unroll 1
+            for (int step = 0; step < 2 * blocks; ++step) {  // 64 keys each
+                const int half = step & 1, i = step >> 1, slot = i & (KPP_SLOTS - 1), k0 = 64 * step;
+                ok = warp_wait(&ct.sfull[tile][half], i & 1, abort, lane);
                 if (!ok)
                     break;
                 tc_fence_after();
-                const int slot = i & (KPP_SLOTS - 1), k0 = i * KPP_KEYS;
-                if (k0 + KPP_KEYS - 1 > all || live < KPP_ROWS)
-                    kpp_mask(t_s, lim - k0);
-                // The row's largest s' = f s + Xv: f is positive and one for 16 keys, so it is that of the
-                // largest s.  The row does not fit the registers twice over; its upper half stays in
-                // them, the lower is read again for the weights.
+                const float4 kf = *reinterpret_cast<const float4 *>(&ct.kf[slot][4 * half]);
+                const float4 xv = *reinterpret_cast<const float4 *>(&ct.xv[slot][4 * half]);
+                const float4 cv = *reinterpret_cast<const float4 *>(&ct.c[slot][4 * half]);
                 uint32_t s[64];
+                tmem_ld64(t_s + 64 * half, s);
+                if (k0 + 63 > all || live < KPP_ROWS) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (k0 + j > lim)
+                            s[j] = 0xFF800000u;
+                }
+                // the largest s' = f s + Xv: f is positive and one for 16 keys, so it is that of the largest s
+                const float f[4] = {kpp_factor(kf.x, qs), kpp_factor(kf.y, qs), kpp_factor(kf.z, qs), kpp_factor(kf.w, qs)};
+                const float x[4] = {xv.x, xv.y, xv.z, xv.w}, c[4] = {cv.x, cv.y, cv.z, cv.w};
                 float m = -INFINITY;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    tmem_ld64(t_s + 64 * half, s);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float top = max3f(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
+                for (int g = 0; g < 4; ++g) {
+                    float t0 = max3f(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]), __uint_as_float(s[16 * g + 2]));
+                    float t1 = max3f(__uint_as_float(s[16 * g + 3]), __uint_as_float(s[16 * g + 4]), __uint_as_float(s[16 * g + 5]));
 #pragma unroll
-                        for (int j = 3; j < 15; j += 2)
-                            top = max3f(top, __uint_as_float(s[16 * g + j]), __uint_as_float(s[16 * g + j + 1]));
-                        top = fmaxf(top, __uint_as_float(s[16 * g + 15]));
-                        m = fmaxf(m, fmaf(top, kpp_factor(ct.kf[slot][4 * half + g], qs), ct.xv[slot][4 * half + g]));
+                    for (int j = 6; j < 14; j += 4) {
+                        t0 = max3f(t0, __uint_as_float(s[16 * g + j]), __uint_as_float(s[16 * g + j + 1]));
+                        t1 = max3f(t1, __uint_as_float(s[16 * g + j + 2]), __uint_as_float(s[16 * g + j + 3]));
                     }
+                    t0 = max3f(t0, __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15]));
+                    m = fmaxf(m, fmaf(fmaxf(t0, t1), f[g], x[g]));
                 }
                 float corr = 1.0f;
                 if (m > M + KPP_LAZY || (M == -INFINITY && m > M)) {
                     corr = ex2(M - m);  // 0 for the first keys
                     M = m;
                 }
-                if (i > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
-                    ok = warp_wait(&ct.odone[tile], (i - 1) & 1, abort, lane);
+                if (step > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
+                    ok = warp_wait(&ct.odone[tile], (step - 1) & 1, abort, lane);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -300,42 +330,37 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 }
                 den *= corr;
                 const float base = M == -INFINITY ? 0.0f : M;
-                // weights 2^(s' - M): the keys of the upper half go to columns 96 .., of the lower to 64 ..,
-                // all of them columns whose scores are in registers
-#pragma unroll 1
-                for (int half = 1; half >= 0; --half) {
-                    if (half == 0)
-                        tmem_ld64(t_s, s);
+                // weights 2^(s' - M), over the scores' columns
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w[16];
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[16];
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const int grp = 4 * half + 2 * q + g;
-                            const float f = kpp_factor(ct.kf[slot][grp], qs), x = ct.xv[slot][grp] - base;
-                            const uint64_t f2 = f2_pack(f, f), x2 = f2_pack(x, x);
-                            uint64_t sum = 0ull;
+                    for (int g = 0; g < 2; ++g) {
+                        const float ff = f[2 * q + g], xx = x[2 * q + g] - base;
+                        const uint64_t f2 = f2_pack(ff, ff), x2 = f2_pack(xx, xx);
+                        uint64_t sum = 0ull;
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                const int e = 32 * q + 16 * g + j;
-                                float a0, a1;
-                                f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, x2), a0, a1);
-                                const float w0 = ex2(a0), w1 = ex2(a1);
-                                sum = f2_add(sum, f2_pack(w0, w1));
-                                w[8 * g + j / 2] = cvt_f16x2(w0, w1);
-                            }
-                            float s0, s1;
-                            f2_unpack(sum, s0, s1);
-                            den = fmaf(s0 + s1, ct.c[slot][grp], den);
+                        for (int j = 0; j < 16; j += 2) {
+                            const int e = 32 * q + 16 * g + j;
+                            float a0, a1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, x2), a0, a1);
+                            const float w0 = ex2(a0), w1 = ex2(a1);
+                            sum = f2_add(sum, f2_pack(w0, w1));
+                            w[8 * g + j / 2] = cvt_f16x2(w0, w1);
                         }
-                        tmem_st16(t_s + 64 + 32 * half + 16 * q, w);
+                        float s0, s1;
+                        f2_unpack(sum, s0, s1);
+                        den = fmaf(s0 + s1, c[2 * q + g], den);
                     }
+                    tmem_st16(t_s + 64 * half + 16 * q, w);
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&ct.pfull[tile]);
+                mbar_arrive(&ct.pfull[tile][half]);
             }
-            if (ok && warp_wait(&ct.odone[tile], (blocks - 1) & 1, abort, lane)) {
+            // the last two products: of the one before, only that it has been issued is known
+            ok = ok && warp_wait(&ct.odone[tile], 0, abort, lane);
+            if (ok && warp_wait(&ct.odone[tile], 1, abort, lane)) {
                 tc_fence_after();
                 const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
                 __nv_bfloat16 *dst =
@@ -373,59 +398,57 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         constexpr int CPR = D / 16, RPP = 128 / CPR, PASSES = KPP_KEYS / RPP;  // 16-byte chunks a row, rows a pass
         const int u = tid - 256, cc = u % CPR, r0 = u / CPR;
         const int32_t *table = a.table + b * a.ld_t;
-        // Lane g holds what concerns the block's keys 16 (g % 8) ..: their page (-1: none) and its scale
-        // bytes.  Table entries are read two blocks ahead, scales and codes one, so that no load waits
-        // for another within a block.
-        auto entry_of = [&](int i) {
-            const int key = i * KPP_KEYS + 16 * (lane & 7);
-            return key < kend ? table[key >> a.shift] : -2;
-        };
-        auto page_of = [&](int entry) {
-            if (entry >= 0 && entry < a.NP)
-                return entry;
-            if (entry != -2 && lane < 8)
-                report_error(FP4LIN_ERR_OUT_OF_RANGE);
-            return -1;
-        };
-        // byte offset of this thread's chunk in each pass, -1 where there is no page; all shuffles
-        // together: one at a time, each waits its turn behind the tensor cores' use of shared memory
-        auto offsets = [&](int pages, int64_t *at) {
-            int page[PASSES];
-#pragma unroll
-            for (int p = 0; p < PASSES; ++p)
-                page[p] = __shfl_sync(0xffffffffu, pages, (r0 + p * RPP) >> 4);
-#pragma unroll
-            for (int p = 0; p < PASSES; ++p)
-                at[p] = page[p] < 0 ? -1
-                                    : ((((int64_t)page[p] * a.H + h) << a.shift) + ((r0 + p * RPP) & P1)) * D + 16 * cc;
-        };
-        auto load = [&](const uint8_t *codes, int i, const int64_t *at, uint4 *x) {
+        // Every thread reads the table entries of its own rows (the same for all threads, or two halves
+        // of them), two blocks ahead, and the codes one block ahead, so that no load waits for another
+        // within a block.  Nothing is exchanged: a shuffle would wait its turn behind the operands that
+        // the tensor cores read from shared memory.
+        auto entries_of = [&](int i, int *e) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                const int key = i * KPP_KEYS + r0 + p * RPP;
-                x[p] = ld_nc_v4_if(codes + at[p], at[p] >= 0 && key < kend);
+                const int key = i * KPP_KEYS + ((r0 + p * RPP) & ~15);
+                e[p] = key < kend ? table[key >> a.shift] : -1;
             }
         };
+        auto load = [&](const uint8_t *codes, int i, const int *e, uint4 *x) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int row = r0 + p * RPP;
+                x[p] = ld_nc_v4_if(codes + ((((int64_t)e[p] * a.H + h) << a.shift) + (row & P1)) * D + 16 * cc,
+                                   (uint32_t)e[p] < (uint32_t)a.NP && i * KPP_KEYS + row < kend);
+            }
+        };
+        // lane g < 8 of the first of these warps: the page of keys 16 g .. and its scale bytes
+        const bool scales = warp == 8 && lane < 8;
+        auto page_of = [&](int i) {
+            const int key = i * KPP_KEYS + 16 * lane;
+            if (!scales || key >= kend)
+                return -1;
+            const int page = table[key >> a.shift];
+            if (page >= 0 && page < a.NP)
+                return page;
+            report_error(FP4LIN_ERR_OUT_OF_RANGE);
+            return -1;
+        };
         uint4 xk[PASSES], xv[PASSES];
-        int pages = page_of(entry_of(0)), entry = entry_of(1);
-        uint32_t kbyte = pages >= 0 ? a.ks[(int64_t)pages * a.H + h] : 0u;
-        uint32_t vbyte = pages >= 0 ? a.vs[(int64_t)pages * a.H + h] : 0u;
-        int64_t at[PASSES];
-        offsets(pages, at);
-        load(a.kc, 0, at, xk);
-        load(a.vc, 0, at, xv);
+        int then[PASSES];
+        entries_of(0, then);
+        load(a.kc, 0, then, xk);
+        load(a.vc, 0, then, xv);
+        entries_of(1, then);
+        int page = page_of(0);
+        uint32_t kbyte = page >= 0 ? a.ks[(int64_t)page * a.H + h] : 0u;
+        uint32_t vbyte = page >= 0 ? a.vs[(int64_t)page * a.H + h] : 0u;
         for (int i = 0; i < blocks; ++i) {
-            const int next = page_of(entry);
-            entry = entry_of(i + 2);
+            const int next = page_of(i + 1);
             const int st = i & 1, par = ((i >> 1) & 1) ^ 1;
             if (i >= 2 && !warp_wait(&ct.kfree[st], par, abort, lane))
                 break;
-            if (warp == 8 && lane < 8) {
+            if (scales) {
                 const int slot = i & (KPP_SLOTS - 1);
                 const float x = vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X;
                 ct.kf[slot][lane] = mxfp8_scale(kbyte);
-                ct.xv[slot][lane] = pages >= 0 ? x : -INFINITY;
-                ct.c[slot][lane] = pages >= 0 ? ex2(-x) : 0.0f;
+                ct.xv[slot][lane] = page >= 0 ? x : -INFINITY;
+                ct.c[slot][lane] = page >= 0 ? ex2(-x) : 0.0f;
             }
             kbyte = next >= 0 ? a.ks[(int64_t)next * a.H + h] : 0u;
             vbyte = next >= 0 ? a.vs[(int64_t)next * a.H + h] : 0u;
@@ -434,10 +457,8 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 kpp_convert<D>(s_k + st * TILE, r0 + p * RPP, cc, xk[p]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&ct.kfull[st]);
-            if (i + 1 < blocks) {
-                offsets(next, at);
-                load(a.kc, i + 1, at, xk);
-            }
+            if (i + 1 < blocks)
+                load(a.kc, i + 1, then, xk);
             if (i >= 2 && !warp_wait(&ct.vfree[st], par, abort, lane))
                 break;
             if ((i + 1) * KPP_KEYS - 1 > all) {  // keys that some rows do not see: weight 0 must stay 0
@@ -456,55 +477,52 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&ct.vfull[st]);
             if (i + 1 < blocks)
-                load(a.vc, i + 1, at, xv);
-            pages = next;
+                load(a.vc, i + 1, then, xv);
+            entries_of(i + 2, then);
+            page = next;
         }
     } else {
         if (warp == 12) {
-            constexpr uint32_t IQK = kpp_idesc(KPP_KEYS, false), IPV = kpp_idesc(D, true);
-            auto scores = [&](int j, int i) {
-                const uint32_t qa = smem_u32(s_q + j * TILE), ka = smem_u32(s_k + (i & 1) * TILE);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                    mma_f16_ss_w(tmem + j * 128, desc_sw128(qa + off), desc_sw128(ka + off), IQK, k > 0);
-                }
-                tc_commit_w(&ct.sfull[j]);
-                mbar_arrive_w(&ct.sfull[j]);  // passes on what kfull released (the page factors)
+            constexpr uint32_t IQK = kpp_idesc(64, false), IPV = kpp_idesc(D, true);
+            const uint64_t dq = desc_sw128(smem_u32(s_q)), dk = desc_sw128(smem_u32(s_k));
+            const uint64_t dv = desc_sw128_mn(smem_u32(s_v), KPP_KEYS * 128);
+            // 64 keys: half a stage, 8 KB into each of its 64-dimension blocks
+            auto scores = [&](int j, int half, int i) {
+                kpp_issue_scores<D>(tmem + j * 128 + half * 64, dq + j * (TILE >> 4),
+                                    dk + ((i & 1) * TILE + half * 64 * 128 >> 4), IQK, &ct.sfull[j][half]);
             };
-            auto values = [&](int j, int i) {
-                const uint32_t va = smem_u32(s_v + (i & 1) * TILE);
-#pragma unroll
-                for (int k = 0; k < KPP_KEYS / 16; ++k)
-                    mma_f16_ts_w(tmem + 256 + j * D, tmem + j * 128 + 64 + 8 * k, desc_sw128_mn(va + k * 2048, KPP_KEYS * 128),
-                                 IPV, i > 0 || k > 0);
-                tc_commit_w(&ct.odone[j]);
-                mbar_arrive_w(&ct.odone[j]);  // and on what vfull released
+            auto values = [&](int j, int half, int i) {
+                kpp_issue_values(tmem + 256 + j * D, tmem + j * 128 + half * 64,
+                                 dv + ((i & 1) * TILE + half * 64 * 128 >> 4), IPV, i > 0 || half > 0, &ct.odone[j]);
             };
             bool ok = warp_poll(&ct.kfull[0], 0, abort, lane);
             if (ok) {
                 tc_fence_after();
-                for (int j = 0; j < tiles; ++j)
-                    scores(j, 0);
+                for (int half = 0; half < 2; ++half)
+                    for (int j = 0; j < tiles; ++j)
+                        scores(j, half, 0);
                 tc_commit_w(&ct.kfree[0]);
             }
             for (int i = 0; ok && i < blocks; ++i) {
                 const int st = i & 1, par = (i >> 1) & 1;
+                const bool more = i + 1 < blocks;
                 ok = warp_poll(&ct.vfull[st], par, abort, lane);
-                if (ok && i + 1 < blocks)
+                if (ok && more)
                     ok = warp_poll(&ct.kfull[st ^ 1], ((i + 1) >> 1) & 1, abort, lane);
-                for (int j = 0; ok && j < tiles; ++j) {
-                    ok = warp_poll(&ct.pfull[j], i & 1, abort, lane);
+#pragma unroll 1
+                for (int turn = 0; ok && turn < 2 * tiles; ++turn) {
+                    const int half = tiles == 2 ? turn >> 1 : turn, j = tiles == 2 ? turn & 1 : 0;
+                    ok = warp_poll(&ct.pfull[j][half], i & 1, abort, lane);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    values(j, i);
-                    if (i + 1 < blocks)
-                        scores(j, i + 1);
+                    values(j, half, i);
+                    if (more)
+                        scores(j, half, i + 1);
                 }
                 if (ok) {
                     tc_commit_w(&ct.vfree[st]);
-                    if (i + 1 < blocks)
+                    if (more)
                         tc_commit_w(&ct.kfree[st ^ 1]);
                 }
             }
