@@ -319,13 +319,16 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     corr = ex2(M - m);  // 0 for the first keys
                     M = m;
                 }
-                if (step > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
+                // The last product is waited for before the output is scaled, and always before the last
+                // weights are given out: the wait after the loop then has one phase only to mean.
+                const bool grown = __any_sync(0xffffffffu, corr != 1.0f);
+                if (step > 0 && (grown || step + 1 == 2 * blocks)) {
                     ok = warp_wait(&ct.odone[tile], (step - 1) & 1, abort, lane);
                     if (!ok)
                         break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < D / 8; ++k)
+                    for (int k = 0; grown && k < D / 8; ++k)
                         tmem_scale8(t_o + 8 * k, corr);
                 }
                 den *= corr;
@@ -358,8 +361,6 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 tc_fence_before();
                 mbar_arrive(&ct.pfull[tile][half]);
             }
-            // the last two products: of the one before, only that it has been issued is known
-            ok = ok && warp_wait(&ct.odone[tile], 0, abort, lane);
             if (ok && warp_wait(&ct.odone[tile], 1, abort, lane)) {
                 tc_fence_after();
                 const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
