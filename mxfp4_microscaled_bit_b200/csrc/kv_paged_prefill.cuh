@@ -11,6 +11,8 @@
 //                    2^8 (the weights stay below 2^8, far inside f16), which is rare.
 //   warps 8-11       load 128 keys of K and V from their pages, a block ahead in registers, and
 //                    write them as f16 (exact) in the 128-byte-swizzled operand layout.
+//   warp 13          waits for what warp 12 needs next and meets it at a named barrier, which costs the
+//                    issue far less than a wait of its own.
 //   warp 12          issues the MMAs: S = Q K^T (both in shared memory, K-major) and O += P V (P from
 //                    TMEM, V as an MN-major operand: its rows are keys, as in the cache).
 // TMEM: scores and weights of the tiles in columns 0 and 128, outputs in 256 and 256 + D.
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 kpp_issue_values(tmem + 256 + j * D, tmem + j * 128 + half * 64,
                                  dv + ((i & 1) * TILE + half * 64 * 128 >> 4), IPV, i > 0 || half > 0, &ct.odone[j]);
             };
-            bool ok = warp_poll(&ct.kfull[0], 0, abort, lane);
+            bool ok = !meet_or(false);
             if (ok) {
                 tc_fence_after();
                 for (int half = 0; half < 2; ++half)
@@ -505,15 +507,11 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 tc_commit_w(&ct.kfree[0]);
             }
             for (int i = 0; ok && i < blocks; ++i) {
-                const int st = i & 1, par = (i >> 1) & 1;
                 const bool more = i + 1 < blocks;
-                ok = warp_poll(&ct.vfull[st], par, abort, lane);
-                if (ok && more)
-                    ok = warp_poll(&ct.kfull[st ^ 1], ((i + 1) >> 1) & 1, abort, lane);
 #pragma unroll 1
-                for (int turn = 0; ok && turn < 2 * tiles; ++turn) {
+                for (int turn = 0; turn < 2 * tiles; ++turn) {
                     const int half = tiles == 2 ? turn >> 1 : turn, j = tiles == 2 ? turn & 1 : 0;
-                    ok = warp_poll(&ct.pfull[j][half], i & 1, abort, lane);
+                    ok = !meet_or(false);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -522,9 +520,9 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                         scores(j, half, i + 1);
                 }
                 if (ok) {
-                    tc_commit_w(&ct.vfree[st]);
+                    tc_commit_w(&ct.vfree[i & 1]);
                     if (more)
-                        tc_commit_w(&ct.kfree[st ^ 1]);
+                        tc_commit_w(&ct.kfree[(i + 1) & 1]);
                 }
             }
             // nothing may be in flight when TMEM goes and the shared memory with it
@@ -532,6 +530,23 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             if (lane == 0)
                 wait_bounded(&ct.drain, 0, abort, false);
             __syncwarp();
+        } else if (warp == 13) {
+            // the waits of the issuing warp, in its order and a step ahead of it
+            bool ok = warp_poll(&ct.kfull[0], 0, abort, lane);
+            ok = !meet_or(!ok);
+            for (int i = 0; ok && i < blocks; ++i) {
+                ok = warp_poll(&ct.vfull[i & 1], (i >> 1) & 1, abort, lane);
+                if (ok && i + 1 < blocks)
+                    ok = warp_poll(&ct.kfull[(i + 1) & 1], ((i + 1) >> 1) & 1, abort, lane);
+#pragma unroll 1
+                for (int turn = 0; turn < 2 * tiles; ++turn) {
+                    const int half = tiles == 2 ? turn >> 1 : turn, j = tiles == 2 ? turn & 1 : 0;
+                    ok = ok && warp_poll(&ct.pfull[j][half], i & 1, abort, lane);
+                    ok = !meet_or(!ok);
+                    if (!ok)
+                        break;
+                }
+            }
         }
     }
     tc_fence_before();
