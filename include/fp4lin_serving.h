@@ -136,13 +136,15 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
  * head j uses kv head j / G:
  *   o = sum_l softmax(scale * q . k_l) v_l over the visible positions.
  *   q: bf16 [T, H*G, D], token stride ld_q (a multiple of 8), T >= cu_new[B];
- *   out: bf16 [T, H*G, D] contiguous; rows of no request are left as they were;
+ *   out: bf16 [T, H*G, D] contiguous, not overlapping any input; rows of no
+ *   request are left as they were;
  *   max_new, max_len: what the host knows of the lengths, n <= max_new and
  *   lens + n <= max_len <= width * P for every request.  A request that breaks
  *   this (or has negative lengths or rows behind T) is skipped, a page outside
  *   [0, num_pages) counts as not visible; both are recorded as
  *   FP4LIN_ERR_OUT_OF_RANGE.
- * D = 64 or 128; 1 <= G <= 16; B * H <= 65535.  Rows of the cache behind a
+ * D = 64 or 128; 1 <= G <= 16; B * H <= 65535; max_new * G <= 524280; scale
+ * bytes as kv_fp8_store writes them (at most 253).  Rows of the cache behind a
  * request's last may hold anything.  Scores, softmax and sums are binary32, the
  * softmax weights rounded to f16.  workspace: at least
  * kv_fp8_attention_workspace_bytes bytes for the same sizes (may be 0, then

@@ -2,20 +2,27 @@
 // same mathematics on tcgen05.
 //
 // Bound by the tensor cores and, as closely, by the exponentials (4 D flops and one exponential a
-// score: at D = 128 a 256 x 128 block of scores takes ~2050 cycles of either).  One CTA an SM takes
+// score: at D = 128 a 256 x 128 block of scores takes ~2050 cycles of either; the softmax's other
+// instructions bring its warps to ~2900).  Two prompts of up to 2048 tokens behind contexts of up to
+// 6143, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 664 us, 810 TFLOP/s, 49% of the measured bf16
+// rate, of which the last, partly filled wave of CTAs costs a sixth.  One CTA an SM takes
 // 256 (token, head) rows of one kv head, as two tiles of 128: while the softmax of one runs, the
 // tensor cores work on the other, and every key block that is converted serves both.
-//   warps 0-3, 4-7   softmax of tile 0, 1: a thread owns a row.  Reads the row's 128 scores from TMEM,
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread owns a row.  Reads 64 of the row's scores from TMEM,
 //                    applies both scales in one multiply-add, writes the f16 weights over the scores
-//                    in TMEM.  The output is rescaled only when the maximum has grown by more than
-//                    2^8 (the weights stay below 2^8, far inside f16), which is rare.
+//                    in TMEM; meanwhile the next 64 are computed into the tile's other buffer (with
+//                    one buffer of 128 the kernel took 799 us).  The output is rescaled only when the
+//                    maximum has grown by more than 2^8 (the weights stay below 2^8, far inside f16),
+//                    which is rare.
 //   warps 8-11       load 128 keys of K and V from their pages, a block ahead in registers, and
 //                    write them as f16 (exact) in the 128-byte-swizzled operand layout.
 //   warp 13          waits for what warp 12 needs next and meets it at a named barrier, which costs the
-//                    issue far less than a wait of its own.
+//                    issue far less than a wait of its own (723 us).
 //   warp 12          issues the MMAs: S = Q K^T (both in shared memory, K-major) and O += P V (P from
 //                    TMEM, V as an MN-major operand: its rows are keys, as in the cache).
-// TMEM: scores and weights of the tiles in columns 0 and 128, outputs in 256 and 256 + D.
+// TMEM: scores and weights of the tiles in columns 0 and 128 (two buffers of 64 keys each), outputs in
+// 256 and 256 + D.  With fewer tiles than SMs, CTAs share a tile's keys and leave their sums to
+// kv_paged_merge_kernel: one request of 32 rows over 32768 keys in 51 us instead of 512.
 #pragma once
 
 #include "kv_paged_attention.cuh"
@@ -191,7 +198,7 @@ __device__ __forceinline__ void kpp_convert(uint8_t *base, int row, int cc, uint
 __device__ __forceinline__ float kpp_factor(float kf, float qs) { return fmaxf(kf * qs, 1.17549435e-38f); }
 
 template <int D>
-__global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a, int min_rows)
+__global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a)
 {
     extern __shared__ uint8_t kpp_raw[];
     uint8_t *sm = kpp_raw + ((1024u - (smem_u32(kpp_raw) & 1023u)) & 1023u);
@@ -205,13 +212,18 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
     const KvPagedRequest rq = kvp_request(a, b);
     const int rows = rq.n * a.G;
     const int row0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * KPP_ROWS;  // longest first
-    if (rows < min_rows || row0 >= rows)
+    if (rows <= a.max_rows || row0 >= rows)
         return;
     const int live = min(KPP_ROWS, rows - row0);
     const int tiles = live > 128 ? 2 : 1;
     const int imin = row0 / a.G, imax = (row0 + live - 1) / a.G;
     const int kend = rq.len + imax + 1;            // keys that the last row sees
-    const int blocks = (kend + KPP_KEYS - 1) / KPP_KEYS;
+    // this split's blocks of keys; all of them where there is one split
+    const int first_block = (int)blockIdx.z * (a.prefill_chunk / KPP_KEYS);
+    const int blocks = min((kend + KPP_KEYS - 1) / KPP_KEYS - first_block, a.prefill_chunk / KPP_KEYS);
+    if (blocks <= 0)
+        return;
+    const int key0 = first_block * KPP_KEYS;
     const int all = rq.len + imin;                 // last key that every row sees
     const int P1 = (1 << a.shift) - 1;
 
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             bool ok = true;
 #pragma unroll 1
             for (int step = 0; step < 2 * blocks; ++step) {  // 64 keys each
-                const int half = step & 1, i = step >> 1, slot = i & (KPP_SLOTS - 1), k0 = 64 * step;
+                const int half = step & 1, i = step >> 1, slot = i & (KPP_SLOTS - 1), k0 = key0 + 64 * step;
                 ok = warp_wait(&ct.sfull[tile][half], i & 1, abort, lane);
                 if (!ok)
                     break;
@@ -365,14 +377,17 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             }
             if (ok && warp_wait(&ct.odone[tile], 1, abort, lane)) {
                 tc_fence_after();
-                const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
+                const bool whole = a.prefill_S == 1;
+                const float inv = !whole ? 1.0f : den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
                 __nv_bfloat16 *dst =
                     a.out + (int64_t)(rq.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
+                float *part = a.prefill_ws + ((((int64_t)bh * gridDim.x + row0 / KPP_ROWS) * a.prefill_S + blockIdx.z) * KPP_ROWS +
+                                              tid) * (D + 4);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
                     float o[32];
                     tmem_ld32(t_o + 32 * k, o);
-                    if (mine)
+                    if (mine && whole) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8) {
                             uint32_t y[4];
@@ -383,16 +398,28 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                                     : "f"(o[j + 2 * e + 1] * inv), "f"(o[j + 2 * e] * inv));
                             st_v4(dst + 32 * k + j, make_uint4(y[0], y[1], y[2], y[3]));
                         }
+                    } else if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4 *>(part + 32 * k + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
                 }
+                if (mine && !whole)
+                    *reinterpret_cast<float2 *>(part + D) = make_float2(M, den);
                 if (ct.nan && mine) {  // a NaN value code among the keys that not every row sees
-                    for (int key = all + 1; key <= lim; ++key) {
+                    const int last = min(lim, key0 + blocks * KPP_KEYS - 1);
+                    for (int key = max(all + 1, key0); key <= last; ++key) {
                         const int page = a.table[b * a.ld_t + (key >> a.shift)];
                         if (page < 0 || page >= a.NP)
                             continue;
                         const uint8_t *v = a.vc + ((((int64_t)page * a.H + h) << a.shift) + (key & P1)) * D;
                         for (int d = 0; d < D; ++d)
-                            if ((v[d] & 127) == 127)
-                                dst[d] = __ushort_as_bfloat16(0x7FC0);
+                            if ((v[d] & 127) == 127) {
+                                if (whole)
+                                    dst[d] = __ushort_as_bfloat16(0x7FC0);
+                                else
+                                    part[d] = __int_as_float(0x7fc00000);
+                            }
                     }
                 }
             }
@@ -408,7 +435,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         auto entries_of = [&](int i, int *e) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
-                const int key = i * KPP_KEYS + ((r0 + p * RPP) & ~15);
+                const int key = key0 + i * KPP_KEYS + ((r0 + p * RPP) & ~15);
                 e[p] = key < kend ? table[key >> a.shift] : -1;
             }
         };
@@ -417,13 +444,13 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             for (int p = 0; p < PASSES; ++p) {
                 const int row = r0 + p * RPP;
                 x[p] = ld_nc_v4_if(codes + ((((int64_t)e[p] * a.H + h) << a.shift) + (row & P1)) * D + 16 * cc,
-                                   (uint32_t)e[p] < (uint32_t)a.NP && i * KPP_KEYS + row < kend);
+                                   (uint32_t)e[p] < (uint32_t)a.NP && key0 + i * KPP_KEYS + row < kend);
             }
         };
         // lane g < 8 of the first of these warps: the page of keys 16 g .. and its scale bytes
         const bool scales = warp == 8 && lane < 8;
         auto page_of = [&](int i) {
-            const int key = i * KPP_KEYS + 16 * lane;
+            const int key = key0 + i * KPP_KEYS + 16 * lane;
             if (!scales || key >= kend)
                 return -1;
             const int page = table[key >> a.shift];
@@ -464,11 +491,11 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 load(a.kc, i + 1, then, xk);
             if (i >= 2 && !warp_wait(&ct.vfree[st], par, abort, lane))
                 break;
-            if ((i + 1) * KPP_KEYS - 1 > all) {  // keys that some rows do not see: weight 0 must stay 0
+            if (key0 + (i + 1) * KPP_KEYS - 1 > all) {  // keys that some rows do not see: weight 0 must stay 0
                 bool nan = false;
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p)
-                    if (i * KPP_KEYS + r0 + p * RPP > all)
+                    if (key0 + i * KPP_KEYS + r0 + p * RPP > all)
                         nan |= drop_nan_codes(xv[p].x) | drop_nan_codes(xv[p].y) | drop_nan_codes(xv[p].z) |
                                drop_nan_codes(xv[p].w);
                 if (nan)

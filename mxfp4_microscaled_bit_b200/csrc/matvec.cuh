@@ -18,7 +18,9 @@
 // asked for, and little to do for each.  A CTA takes 128 weight rows, 16 a warp, and a slice of K; the
 // CTAs that share rows form a cluster (at most 8) along K.  The partial sums of a row go to one CTA of
 // the cluster through distributed shared memory and are added in a fixed order: one launch, no
-// workspace, the same bits every time.
+// workspace, the same bits every time.  Between launches of a graph: NVFP4, one rotated row, 4096 x 4096
+// 5.1 us; five rows, 4096 x 14336 13.0 us (2.5 TB/s); MXFP4, sixteen 8-bit rows, 14336 x 4096 22.6 us, where
+// the eight warps of a CTA each turn the same x fragments and the CTAs do not fill the SMs evenly.
 #pragma once
 
 #include <cooperative_groups.h>

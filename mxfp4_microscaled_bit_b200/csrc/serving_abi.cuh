@@ -63,16 +63,23 @@ cudaError_t launch_norm(const NormShape &a, int sms, cudaStream_t s)
 
 // ------------------------------------------------------------------ attention
 // Requests of at most KVP_SPLIT_ROWS (token, head) rows are the split kernel's, which streams the
-// cache at HBM speed; the others the tensor-core kernel's.
+// cache at HBM speed; the others the tensor-core kernel's.  With 32 or 64 in its place, which makes the
+// split kernel read the cache once for every 16 rows (us for 16 / 32 / 64; 8 kv heads, D = 128):
+// 32 requests of 32 rows over 4096 keys 163 / 234 / 234, 64 of 20 rows 319 / 433 / 433, one of 32 rows
+// over 32768 keys 53 / 81 / 81, 16 of 32 rows over 600 keys 22 / 58 / 58; only one of 32 rows over
+// 2048 keys is better off there, 24 / 15 / 15.
 constexpr int KVP_SPLIT_ROWS = 16;
 
 struct KvPagedPlan {
     int nt, rows, tiles, chunk, S, max_rows;
     int prefill_tiles;  // 0: no request can have more than KVP_SPLIT_ROWS rows
-    size_t ws_bytes;
+    int prefill_chunk, prefill_S;
+    size_t split_bytes, ws_bytes;  // the split kernel's share, and all
 };
 
-// Keys a CTA: enough CTAs for several on every SM, in multiples of a step of the CTA's warps.
+// Keys a CTA: enough CTAs for several on every SM, in multiples of a step of the CTA's warps, at most
+// KVP_MAX_CHUNK (32 ragged requests of up to 32768 keys, 8 heads: 300 us with 1024, 278 with 2048, 287 with
+// 4096).
 KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D, int sms)
 {
     KvPagedPlan p{};
@@ -93,7 +100,21 @@ KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D,
     p.chunk = (int)chunk;
     p.S = (int)((max_len + chunk - 1) / chunk);
     // up to 8 splits are one cluster, joined in the kernel; more leave their parts in the workspace
-    p.ws_bytes = p.S > 8 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
+    p.split_bytes = p.S > 8 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
+    p.ws_bytes = p.split_bytes;
+    if (p.prefill_tiles) {
+        // a CTA an SM; with fewer tiles the keys are shared, at least 4 blocks to a CTA.  With at least
+        // 2 / 3 / 4 / 8 / 16 blocks, and unshared (8 kv heads, D = 128): one request of 32 rows over 8192
+        // keys 28 / 29 / 27 / 34 / 47 / 136 us, one of 512 rows over 4096 keys 38 / 34 / 36 / 43 / 61 / 91,
+        // one of 256 over 2048 27 / 30 / 31 / 40 / 55 / 54, one of 32 over 32768 51 / 53 / 51 / 51 / 54 / 512
+        const int64_t tiles = (int64_t)B * H * p.prefill_tiles, blocks = (max_len + KPP_KEYS - 1) / KPP_KEYS;
+        int64_t S = std::max<int64_t>(1, std::min(sms / tiles, blocks / 4));
+        const int64_t per = (blocks + S - 1) / S;
+        p.prefill_S = (int)((blocks + per - 1) / per);
+        p.prefill_chunk = (int)per * KPP_KEYS;
+        if (p.prefill_S > 1)
+            p.ws_bytes += (size_t)tiles * p.prefill_S * KPP_ROWS * (D + 4) * sizeof(float);
+    }
     return p;
 }
 
@@ -109,8 +130,15 @@ template <int D>
 cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream_t s)
 {
     if (p.prefill_tiles) {
-        const cudaError_t e = launch_pdl(kv_paged_prefill_kernel<D>, dim3((unsigned)p.prefill_tiles, (unsigned)(a.B * a.H)),
-                                         dim3(KPP_THREADS), kpp_smem(D), s, a, p.max_rows + 1);
+        cudaError_t e = launch_pdl(kv_paged_prefill_kernel<D>,
+                                   dim3((unsigned)p.prefill_tiles, (unsigned)(a.B * a.H), (unsigned)p.prefill_S),
+                                   dim3(KPP_THREADS), kpp_smem(D), s, a);
+        if (e == cudaSuccess && p.prefill_S > 1) {
+            const KvPagedParts parts{a.prefill_ws, KPP_ROWS, p.prefill_tiles, p.prefill_S, p.prefill_chunk, p.max_rows,
+                                     0x7FFFFFFF};
+            const dim3 mgrid((unsigned)(((int64_t)a.max_new * a.G + 3) / 4), (unsigned)(a.B * a.H));
+            e = launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, parts);
+        }
         if (e != cudaSuccess)
             return e;
     }
@@ -131,7 +159,8 @@ cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream
     if (e != cudaSuccess || p.S <= 8)
         return e;
     const dim3 mgrid((unsigned)((std::min<int64_t>((int64_t)a.max_new * a.G, p.max_rows) + 3) / 4), (unsigned)(a.B * a.H));
-    return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, p.rows);
+    return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a,
+                      KvPagedParts{a.ws, p.rows, p.tiles, p.S, p.chunk, 0, p.max_rows});
 }
 
 // ------------------------------------------------------------------ matvec
@@ -456,6 +485,9 @@ int kv_fp8_attention(const void *q, int64_t ld_q, int T, const uint8_t *k_codes,
     a.tiles = p.tiles;
     a.max_rows = p.max_rows;
     a.joined = p.S > 1 && p.S <= 8;
+    a.prefill_ws = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + p.split_bytes);
+    a.prefill_chunk = p.prefill_chunk;
+    a.prefill_S = p.prefill_S;
     if (p.prefill_tiles) {
         int ordinal = 0;
         if (cudaGetDevice(&ordinal) != cudaSuccess)

@@ -260,8 +260,8 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
     pf = _arg(fn, "free_pages", free_pages, _I32, 1, dev)
     ph = _arg(fn, "free_head", free_head, _I32, 1, dev)
     made = []
-    if max_tokens < 1:
-        raise ValueError(f"{fn}: max_tokens must be at least 1, not {max_tokens}")
+    if not 1 <= max_tokens < 2 ** 31:
+        raise ValueError(f"{fn}: max_tokens must be at least 1 and below 2^31, not {max_tokens}")
     if cu_new is None:
         cu_new = _empty_strided((B + 1,), (1,), _I32)
         made.append(cu_new)
@@ -353,6 +353,8 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
         made.append(out)
     else:
         _arg(fn, "out", out, _BF16, T * HQ * D, dev)
+    if not (1 <= max_new < 2 ** 31 and 1 <= max_len < 2 ** 31):
+        raise ValueError(f"{fn}: max_new and max_len must be at least 1 and below 2^31, not {max_new} and {max_len}")
     L, G = _lib(), HQ // H
     if workspace is None:
         need = L.kv_fp8_attention_workspace_bytes(B, H, G, max_new, max_len, D)

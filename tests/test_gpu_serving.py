@@ -488,6 +488,65 @@ def test_attention_split_counts(L):
     status_ok()
 
 
+@pytest.mark.parametrize("B,H,G,D,P,lens,new,max_len", [
+    (1, 2, 8, 128, 64, [2046], [4], None),             # the last key of a block
+    (1, 1, 8, 64, 16, [2047], [5], None),              # and a block more, with four keys in it
+    (2, 1, 4, 128, 32, [5000, 40], [70, 5], None),     # requests of fewer splits, and of one
+    (2, 1, 4, 64, 128, [2900, 3100], [100, 3], 9000),  # splits that no request reaches; a tile of 144 rows
+    (3, 1, 8, 128, 64, [6000, 6100, 0], [40, 1, 0], None),  # beside a single token's split kernel and its merge
+    (1, 1, 1, 64, 16, [0], [2500], None)])             # rows whose first split has keys and whose later ones none
+def test_attention_many_rows_with_the_keys_split(B, H, G, D, P, lens, new, max_len):
+    q, caches, table, lens, cu = attention_case(B, H, G, D, P, lens, new, seed=H + G + D + P)
+    table = np.pad(table, ((0, 0), (0, max(0, (max_len or 0) // P + 1 - table.shape[1]))), constant_values=-1)
+    attention_check(q, caches, table, lens, cu, P, max_len=max_len)
+    status_ok()
+
+
+def test_attention_nan_values_and_missing_pages_where_the_keys_are_split():
+    q, caches, table, lens, cu = attention_case(1, 1, 8, 64, 16, [4000], [60], seed=4)
+    (kc, kb), (vc, vb) = caches
+    vc[table[0, 5], 0, 3, 7] = 0x7F                  # a key that all rows see
+    vc[table[0, 4030 // 16], 0, 4030 % 16, 9] = 0xFF  # one that the last 30 tokens see
+    out = torch.empty(q.shape, dtype=torch.bfloat16, device=DEV)
+    a = [(u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu)]
+    fl.kv_fp8_attention(q.to(DEV), *a, max_new=60, max_len=4060, out=out)
+    got = torch.isnan(out[:60]).cpu()
+    want = torch.zeros_like(got)
+    want[:, :, 7] = True
+    want[30:, :, 9] = True
+    assert torch.equal(got, want)
+    status_ok()
+    table[0, 128:] = -1  # whole splits without a page
+    a[2] = gpu(table)
+    fl.kv_fp8_attention(q.to(DEV), *a, max_new=60, max_len=4060, out=out)
+    assert fl.device_status() == OUT_OF_RANGE
+    t64 = ref.attention(ref.f64(q), kc, kb, vc, vb, table, lens, cu, 16, 64 ** -0.5)[0][:60]
+    have = ~np.isnan(t64)
+    assert np.abs(ref.f64(out)[:60][have] - t64[have]).max() < 0.05
+    assert torch.isnan(out[:60, :, 7]).all() and not torch.isnan(out[:60, :, 8:]).any()
+
+
+def test_attention_many_rows_over_and_over():
+    """Short and long contexts back to back, each with the same bits every time: no wait depends on luck."""
+    for D, lens, new in ((64, [0, 100, 300, 0], [300, 40, 256, 33]), (128, [60, 1000, 0, 129], [129, 300, 64, 512])):
+        q, caches, table, lens, cu = attention_case(4, 2, 2, D, 32, lens, new, seed=D)
+        (kc, kb), (vc, vb) = caches
+        a = [q.to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu)]
+        kw = dict(max_new=max(new), max_len=int((lens + np.asarray(new)).max()))
+        first = fl.kv_fp8_attention(*a, **kw)
+        other = torch.cuda.Stream()
+        other.wait_stream(torch.cuda.current_stream())
+        T = int(cu[-1])
+        same = torch.ones((), dtype=torch.bool, device=DEV)
+        for k in range(400):
+            out = fl.kv_fp8_attention(*a, **kw)
+            fl.kv_fp8_attention(*a, **kw, stream=other)  # and beside itself
+            same &= (out[:T].view(torch.int16) == first[:T].view(torch.int16)).all()
+        torch.cuda.synchronize()
+        assert bool(same)
+        status_ok()
+
+
 def test_attention_skips_and_reports_what_breaks_its_bounds():
     q, caches, table, lens, cu = attention_case(3, 1, 2, 64, 16, [20, 40, 3], [2, 3, 1], seed=2)
     (kc, kb), (vc, vb) = caches
