@@ -29,6 +29,8 @@ constexpr int KVP_MAX_CHUNK = 2048;    // keys a CTA
 constexpr int KVP_STEP = 32;           // keys a warp takes at a time
 constexpr float KVP_ZERO_X = -8.0f;
 
+struct KppJob;
+
 struct KvPagedShape {
     const __nv_bfloat16 *q;  // [T, H*G, D], token stride ld_q
     const uint8_t *kc, *ks, *vc, *vs;
@@ -41,8 +43,9 @@ struct KvPagedShape {
     int chunk, S, tiles;
     bool joined;             // the S splits of a tile are one cluster
     int max_rows;            // requests of more rows are the tensor-core kernel's (kv_paged_prefill.cuh)
-    float *prefill_ws;       // its [B*H, tiles, S, rows, D + 4], where it splits the keys
-    int prefill_chunk, prefill_S;
+    int4 *prefill_ws;        // its workspace
+    KppJob *prefill_jobs;
+    int prefill_most, sms;   // its tiles, at most
 };
 
 // One request as a CTA sees it; ok is false where the lengths cannot be what the caller promised
@@ -469,69 +472,87 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
     cl.sync();  // no CTA leaves while it is read
 }
 
-// The splits that one of the two kernels left: of tiles of R rows, for requests of more than lo and at
-// most hi rows.
-struct KvPagedParts {
-    const float *ws;
-    int R, tiles, S, chunk, lo, hi;
-};
-
-// Joins a row's splits: o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) den_s.  One warp a row.
-template <int D>
-__global__ void __launch_bounds__(128) kv_paged_merge_kernel(KvPagedShape a, KvPagedParts parts)
+// Joins a row's splits: o = sum_s 2^(M_s - M) o_s / sum_s 2^(M_s - M) den_s, by one warp, or, where there
+// are many, by the CTA, whose warps take every KVP_WARPS-th and then meet.  src: the row's first split,
+// `step` floats from one to the next.
+template <int D, bool CTA>
+__device__ __forceinline__ void kvp_merge_row(const float *src, int64_t step, int splits, __nv_bfloat16 *dst)
 {
-    const int R = parts.R;
-    const int lane = threadIdx.x & 31;
-    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
-    const int rho = blockIdx.x * 4 + (threadIdx.x >> 5);
-    pdl_wait();
-    const KvPagedRequest rq = kvp_request(a, b);
-    const int rows = rq.n * a.G;
-    if (rho >= rows || rows <= parts.lo || rows > parts.hi)
-        return;
-    const int z = rho / R, r = rho - z * R, i = rho / a.G, j = rho - i * a.G;
-    const int imax = (min((z + 1) * R, rows) - 1) / a.G;
-    const int splits = (rq.len + imax + parts.chunk) / parts.chunk;  // ceil((len + imax + 1) / chunk)
-    const int64_t step = (int64_t)R * (D + 4);
-    const float *src = parts.ws + (((int64_t)bh * parts.tiles + z) * parts.S * R + r) * (D + 4);
-    float M = -INFINITY;
-    for (int s = lane; s < splits; s += 32)
+    constexpr int V = D / 32, W = CTA ? KVP_WARPS : 1;
+    __shared__ float part[KVP_WARPS][D + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s0 = CTA ? warp : 0;
+    float M = -INFINITY, den = 0.0f, v[V] = {};
+    for (int s = s0 + W * lane; s < splits; s += 32 * W)
         M = fmaxf(M, src[s * step + D]);
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.0f : M;
-    float den = 0.0f, v[D / 32];
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k)
-        v[k] = 0.0f;
-    for (int s = 0; s < splits; ++s) {
+#pragma unroll 4
+    for (int s = s0; s < splits; s += W) {
         const float *p = src + s * step;
         const float2 md = *reinterpret_cast<const float2 *>(p + D);
         const float f = ex2(md.x - base);
         den = fmaf(f, md.y, den);
-        if constexpr (D == 128) {
-            const float4 x = *reinterpret_cast<const float4 *>(p + lane * 4);
-            v[0] = fmaf(f, x.x, v[0]);
-            v[1] = fmaf(f, x.y, v[1]);
-            v[2] = fmaf(f, x.z, v[2]);
-            v[3] = fmaf(f, x.w, v[3]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2 *>(p + lane * 2);
-            v[0] = fmaf(f, x.x, v[0]);
-            v[1] = fmaf(f, x.y, v[1]);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(p + lane * V + k);
+            v[k] = fmaf(f, x.x, v[k]);
+            v[k + 1] = fmaf(f, x.y, v[k + 1]);
         }
     }
-    const float inv = den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
-    uint32_t y[D / 64];
+    auto inverse = [](float d) { return d > 0.0f ? __fdiv_rn(1.0f, d) : d == 0.0f ? 0.0f : d; };
+    if constexpr (!CTA) {
+        const float inv = inverse(den);
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y[k]) : "f"(v[2 * k + 1] * inv), "f"(v[2 * k] * inv));
-    __nv_bfloat16 *dst = a.out + ((int64_t)(rq.first + i) * a.H * a.G + h * a.G + j) * D;
-    if constexpr (D == 128)
-        *reinterpret_cast<uint2 *>(dst + lane * 4) = make_uint2(y[0], y[1]);
-    else
-        *reinterpret_cast<uint32_t *>(dst + lane * 2) = y[0];
+        for (int k = 0; k < V; k += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(dst + lane * V + k) = __floats2bfloat162_rn(v[k] * inv, v[k + 1] * inv);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            part[warp][lane * V + k] = v[k];
+        if (lane == 0) {
+            part[warp][D] = M;
+            part[warp][D + 1] = den;
+        }
+        __syncthreads();
+        float f[KVP_WARPS], top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < KVP_WARPS; ++w)
+            top = fmaxf(top, part[w][D]);
+        den = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KVP_WARPS; ++w) {
+            f[w] = ex2(part[w][D] - (top == -INFINITY ? 0.0f : top));
+            den = fmaf(f[w], part[w][D + 1], den);
+        }
+        const float inv = inverse(den);
+        for (int d = threadIdx.x; d < D; d += KVP_THREADS) {
+            float o = 0.0f;
+#pragma unroll
+            for (int w = 0; w < KVP_WARPS; ++w)
+                o = fmaf(f[w], part[w][d], o);
+            dst[d] = __float2bfloat16_rn(o * inv);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(KVP_THREADS) kv_paged_merge_kernel(KvPagedShape a, int R)
+{
+    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H, rho = blockIdx.x;
+    pdl_wait();
+    const KvPagedRequest rq = kvp_request(a, b);
+    const int rows = rq.n * a.G;
+    if (rho >= rows || rows > a.max_rows)
+        return;
+    const int z = rho / R, r = rho - z * R, i = rho / a.G, j = rho - i * a.G;
+    const int imax = (min((z + 1) * R, rows) - 1) / a.G;
+    const int splits = (rq.len + imax + a.chunk) / a.chunk;  // ceil((len + imax + 1) / chunk)
+    const float *src = a.ws + (((int64_t)bh * a.tiles + z) * a.S * R + r) * (D + 4);
+    kvp_merge_row<D, true>(src, (int64_t)R * (D + 4), splits,
+                           a.out + ((int64_t)(rq.first + i) * a.H * a.G + h * a.G + j) * D);
 }
 
 }  // namespace fp4lin

@@ -4,10 +4,10 @@
 // Bound by the tensor cores and, as closely, by the exponentials (4 D flops and one exponential a
 // score: at D = 128 a 256 x 128 block of scores takes ~2050 cycles of either; the softmax's other
 // instructions bring its warps to ~2900).  Two prompts of up to 2048 tokens behind contexts of up to
-// 6143, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 664 us, 810 TFLOP/s, 49% of the measured bf16
-// rate, of which the last, partly filled wave of CTAs costs a sixth.  One CTA an SM takes
-// 256 (token, head) rows of one kv head, as two tiles of 128: while the softmax of one runs, the
-// tensor cores work on the other, and every key block that is converted serves both.
+// 8191, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 636 us, 850 TFLOP/s, 51% of the measured bf16
+// rate.  One CTA an SM takes 256 (token, head) rows of one kv head, as two tiles of 128: while the
+// softmax of one runs, the tensor cores work on the other, and every key block that is converted serves
+// both.
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread owns a row.  Reads 64 of the row's scores from TMEM,
 //                    applies both scales in one multiply-add, writes the f16 weights over the scores
 //                    in TMEM; meanwhile the next 64 are computed into the tile's other buffer (with
@@ -21,9 +21,16 @@
 //   warp 12          issues the MMAs: S = Q K^T (both in shared memory, K-major) and O += P V (P from
 //                    TMEM, V as an MN-major operand: its rows are keys, as in the cache).
 // TMEM: scores and weights of the tiles in columns 0 and 128 (two buffers of 64 keys each), outputs in
-// 256 and 256 + D.  With fewer tiles than SMs, CTAs share a tile's keys and leave their sums to
-// kv_paged_merge_kernel: one request of 32 rows over 32768 keys in 51 us instead of 512.
+// 256 and 256 + D.
+//
+// Which tiles there are is known on the device only: kv_paged_plan_kernel lists them, and this kernel's
+// grid has as many CTAs as T tokens can need.  (A grid over every request's longest case spent 130 us
+// more where one prompt of 2048 tokens came with 63 decoding requests.)  Where there are few tiles, and at
+// the end of many, CTAs share a tile's keys (kpp_split) and leave their sums to
+// kv_paged_prefill_merge_kernel: one request of 32 rows over 32768 keys takes 51 us instead of 512.
 #pragma once
+
+#include <type_traits>
 
 #include "kv_paged_attention.cuh"
 
@@ -33,6 +40,8 @@ constexpr int KPP_THREADS = 512;
 constexpr int KPP_KEYS = 128;          // keys a block
 constexpr int KPP_ROWS = 256;          // rows a CTA
 constexpr int KPP_SLOTS = 4;           // blocks whose page factors are held at once
+constexpr int KPP_MIN_BLOCKS = 4;      // blocks of keys to a CTA, at least (one request of 512 rows over 4096
+                                       // keys: 2 / 3 / 4 / 8 / 16 take 38 / 34 / 36 / 43 / 61 us)
 constexpr float KPP_LAZY = 8.0f;       // log2 growth of the maximum that is let pass
 
 struct KppCtrl {
@@ -41,6 +50,50 @@ struct KppCtrl {
     uint32_t tmem;
     int abort, nan;
 };
+
+// How `alive` tiles become CTAs: the last `tail` of them are `parts` CTAs each.  Up to half a GPU's worth
+// is shared so that it fills the GPU, up to two thirds by three; one to a CTA leaves less than a third
+// idle above that; of more than a GPU's worth, a quarter of that by four, which evens out the last wave
+// (464 tiles of 52 to 80 blocks of keys: 683 us without).
+struct KppSplit {
+    int tail, parts;
+};
+
+__host__ __device__ inline KppSplit kpp_split(int alive, int sms)
+{
+    if (alive <= sms / 2)
+        return {alive, alive ? sms / alive : 1};
+    if (alive <= 2 * sms / 3)
+        return {alive, 3};
+    if (alive <= sms)
+        return {0, 1};
+    return {sms / 4, 4};
+}
+
+// The most CTAs that up to `most` tiles can become, and of them those that share a tile.
+inline int64_t kpp_grid(int64_t most, int sms)
+{
+    return most <= sms / 2 ? sms : most <= sms ? 2 * sms : most + 3 * (sms / 4);
+}
+inline int64_t kpp_parts(int64_t most, int sms) { return most <= sms / 2 ? sms : 2 * (int64_t)sms; }
+
+// A CTA's work: head bh's rows from row0 on (of a request with `len` rows in the cache and its first
+// token at `first`), `blocks` blocks of keys from key0 on; sums: its place among the sums where the tile
+// is shared, else -1.
+struct alignas(16) KppJob {
+    int bh, row0, key0, blocks, sums, len, first, live;
+};
+
+// Workspace, in units of 16 bytes: a header (jobs, tail tiles, parts); for each shared tile its bh, first
+// row, rows and number of splits; the sums [tile, part, row, D + 4]; the jobs.
+inline int64_t kpp_jobs_at(int64_t most, int sms, int D)
+{
+    return 1 + sms + kpp_parts(most, sms) * KPP_ROWS * (D + 4) / 4;
+}
+inline size_t kpp_workspace(int64_t most, int sms, int D)
+{
+    return 16 * (size_t)kpp_jobs_at(most, sms, D) + sizeof(KppJob) * (size_t)kpp_grid(most, sms);
+}
 
 constexpr size_t kpp_smem(int D) { return 1024 + (size_t)(KPP_ROWS + 4 * KPP_KEYS) * D * 2 + sizeof(KppCtrl); }
 
@@ -197,6 +250,77 @@ __device__ __forceinline__ void kpp_convert(uint8_t *base, int row, int cc, uint
 // the -inf of a masked score stays one.
 __device__ __forceinline__ float kpp_factor(float kf, float qs) { return fmaxf(kf * qs, 1.17549435e-38f); }
 
+// The CTAs' work from the requests' lengths.  One CTA: a thread counts the tiles of a range of requests,
+// the block adds them up, and then each thread looks up its jobs' requests.
+constexpr int KPP_PLAN_THREADS = 1024;
+
+__global__ void __launch_bounds__(KPP_PLAN_THREADS) kv_paged_plan_kernel(KvPagedShape a)
+{
+    __shared__ int upto_of[KPP_PLAN_THREADS], warp_sum[KPP_PLAN_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    const int per = (a.B + KPP_PLAN_THREADS - 1) / KPP_PLAN_THREADS;
+    auto tiles_of = [&](int r) {
+        const int n = kvp_request(a, r).n * a.G;
+        return n > a.max_rows ? (n + KPP_ROWS - 1) / KPP_ROWS * a.H : 0;
+    };
+    int upto = 0;
+    for (int r = tid * per; r < min(tid * per + per, a.B); ++r)
+        upto += tiles_of(r);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        upto += lane >= o ? y : 0;
+    }
+    if (lane == 31)
+        warp_sum[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        upto += warp_sum[w];
+    upto_of[tid] = upto;
+    __syncthreads();
+    // more than prefill_most only where offsets fall, which is an error anyway
+    const int alive = min(upto_of[KPP_PLAN_THREADS - 1], a.prefill_most);
+    const KppSplit sp = kpp_split(alive, a.sms);
+    const int alone = alive - sp.tail, jobs = alone + sp.tail * sp.parts;
+    if (tid == 0)
+        a.prefill_ws[0] = make_int4(jobs, sp.tail, sp.parts, 0);
+    for (int j = tid; j < jobs; j += KPP_PLAN_THREADS) {
+        const int shared = j < alone ? -1 : (j - alone) / sp.parts, parts = shared < 0 ? 1 : sp.parts;
+        const int part = shared < 0 ? 0 : j - alone - shared * parts;
+        int t = shared < 0 ? j : alone + shared;
+        int lo = 0, hi = KPP_PLAN_THREADS - 1;  // the first range that ends behind t
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (upto_of[mid] > t)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        t -= lo ? upto_of[lo - 1] : 0;
+        int b = lo * per;
+        for (int n; (n = tiles_of(b)) <= t; ++b)
+            t -= n;
+        const KvPagedRequest rq = kvp_request(a, b);
+        const int rows = rq.n * a.G, of_head = (rows + KPP_ROWS - 1) / KPP_ROWS, h = t / of_head;
+        KppJob job;
+        job.bh = b * a.H + h;
+        job.row0 = (of_head - 1 - (t - h * of_head)) * KPP_ROWS;  // longest first
+        job.live = min(KPP_ROWS, rows - job.row0);
+        job.len = rq.len;
+        job.first = rq.first;
+        // the blocks of keys that the tile's last row sees, and this CTA's share of them
+        const int blocks = (rq.len + (job.row0 + job.live - 1) / a.G + KPP_KEYS) / KPP_KEYS;
+        const int chunk = max((blocks + parts - 1) / parts, KPP_MIN_BLOCKS);
+        job.key0 = part * chunk * KPP_KEYS;
+        job.blocks = max(0, min(blocks - part * chunk, chunk));
+        job.sums = blocks > chunk ? shared * parts + part : -1;
+        if (shared >= 0 && part == 0)
+            a.prefill_ws[1 + shared] = make_int4(job.bh, job.row0, job.live, (blocks + chunk - 1) / chunk);
+        a.prefill_jobs[j] = job;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPagedShape a)
 {
@@ -207,24 +331,19 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
     KppCtrl &ct = *reinterpret_cast<KppCtrl *>(sm + 6 * TILE);
     volatile int *abort = &ct.abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
     pdl_wait();
-    const KvPagedRequest rq = kvp_request(a, b);
-    const int rows = rq.n * a.G;
-    const int row0 = ((int)gridDim.x - 1 - (int)blockIdx.x) * KPP_ROWS;  // longest first
-    if (rows <= a.max_rows || row0 >= rows)
+    KppJob job = a.prefill_jobs[blockIdx.x];
+    // one value for the warp: the compiler may keep them, and addresses made of them, in uniform registers
+    job.bh = __reduce_min_sync(0xffffffffu, job.bh);
+    job.row0 = __reduce_min_sync(0xffffffffu, job.row0);
+    job.key0 = __reduce_min_sync(0xffffffffu, job.key0);
+    if ((int)blockIdx.x >= a.prefill_ws[0].x || job.blocks == 0)
         return;
-    const int live = min(KPP_ROWS, rows - row0);
+    const int b = job.bh / a.H, h = job.bh - b * a.H, row0 = job.row0, live = job.live, len = job.len;
+    const int key0 = job.key0, blocks = job.blocks;
     const int tiles = live > 128 ? 2 : 1;
-    const int imin = row0 / a.G, imax = (row0 + live - 1) / a.G;
-    const int kend = rq.len + imax + 1;            // keys that the last row sees
-    // this split's blocks of keys; all of them where there is one split
-    const int first_block = (int)blockIdx.z * (a.prefill_chunk / KPP_KEYS);
-    const int blocks = min((kend + KPP_KEYS - 1) / KPP_KEYS - first_block, a.prefill_chunk / KPP_KEYS);
-    if (blocks <= 0)
-        return;
-    const int key0 = first_block * KPP_KEYS;
-    const int all = rq.len + imin;                 // last key that every row sees
+    const int kend = len + (row0 + live - 1) / a.G + 1;  // keys that the last row sees
+    const int all = len + row0 / a.G;                    // last key that every row sees
     const int P1 = (1 << a.shift) - 1;
 
     if (tid == 0) {
@@ -256,7 +375,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
     const bool mine = tid < live;
     if (warp < 8) {
         const __nv_bfloat16 *src =
-            a.q + (int64_t)(rq.first + (mine ? tok : 0)) * a.ld_q + (int64_t)(h * a.G + (mine ? head : 0)) * D;
+            a.q + (int64_t)(job.first + (mine ? tok : 0)) * a.ld_q + (int64_t)(h * a.G + (mine ? head : 0)) * D;
         float m = 0.0f;
         for (int i = 0; i < D / 8; ++i) {
             float f[8];
@@ -291,7 +410,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         if (tile < tiles) {
             const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
             const uint32_t t_s = tmem + lanes + tile * 128, t_o = tmem + lanes + 256 + tile * D;
-            const int lim = mine ? rq.len + tok : -1;
+            const int lim = mine ? len + tok : -1;
             float M = -INFINITY, den = 0.0f;
             bool ok = true;
 #pragma unroll 1
@@ -377,12 +496,12 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             }
             if (ok && warp_wait(&ct.odone[tile], 1, abort, lane)) {
                 tc_fence_after();
-                const bool whole = a.prefill_S == 1;
+                const bool whole = job.sums < 0;
                 const float inv = !whole ? 1.0f : den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
                 __nv_bfloat16 *dst =
-                    a.out + (int64_t)(rq.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
-                float *part = a.prefill_ws + ((((int64_t)bh * gridDim.x + row0 / KPP_ROWS) * a.prefill_S + blockIdx.z) * KPP_ROWS +
-                                              tid) * (D + 4);
+                    a.out + (int64_t)(job.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
+                float *sums = reinterpret_cast<float *>(a.prefill_ws + 1 + a.sms) +
+                              ((int64_t)job.sums * KPP_ROWS + tid) * (D + 4);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
                     float o[32];
@@ -401,11 +520,11 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     } else if (mine) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(part + 32 * k + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            *reinterpret_cast<float4 *>(sums + 32 * k + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                 }
                 if (mine && !whole)
-                    *reinterpret_cast<float2 *>(part + D) = make_float2(M, den);
+                    *reinterpret_cast<float2 *>(sums + D) = make_float2(M, den);
                 if (ct.nan && mine) {  // a NaN value code among the keys that not every row sees
                     const int last = min(lim, key0 + blocks * KPP_KEYS - 1);
                     for (int key = max(all + 1, key0); key <= last; ++key) {
@@ -418,7 +537,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                                 if (whole)
                                     dst[d] = __ushort_as_bfloat16(0x7FC0);
                                 else
-                                    part[d] = __int_as_float(0x7fc00000);
+                                    sums[d] = __int_as_float(0x7fc00000);
                             }
                     }
                 }
@@ -582,6 +701,34 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+}
+
+// Rows of the shared tile blockIdx.y, 1 or KVP_WARPS to a CTA: a warp each, or, where few tiles have many
+// parts, the whole CTA for one after the other.
+template <int D>
+__global__ void __launch_bounds__(KVP_THREADS) kv_paged_prefill_merge_kernel(KvPagedShape a)
+{
+    pdl_wait();
+    const int4 head = a.prefill_ws[0], t = a.prefill_ws[1 + blockIdx.y];
+    if ((int)blockIdx.y >= head.y || t.w < 2)
+        return;
+    const int b = t.x / a.H, h = t.x - b * a.H;
+    const int64_t first = a.cu[b];
+    auto join = [&](auto cta, int r) {
+        if (r >= t.z)
+            return;
+        const int rho = t.y + r, i = rho / a.G, j = rho - i * a.G;
+        const float *src = reinterpret_cast<const float *>(a.prefill_ws + 1 + a.sms) +
+                           ((int64_t)blockIdx.y * head.z * KPP_ROWS + r) * (D + 4);
+        kvp_merge_row<D, decltype(cta)::value>(src, (int64_t)KPP_ROWS * (D + 4), t.w,
+                                               a.out + ((first + i) * a.H * a.G + h * a.G + j) * D);
+    };
+    const int per = KPP_ROWS / gridDim.x, r = blockIdx.x * per;
+    if (per == KVP_WARPS && t.w <= 8)
+        join(std::false_type{}, r + (threadIdx.x >> 5));
+    else
+        for (int k = 0; k < per; ++k)
+            join(std::true_type{}, r + k);
 }
 
 }  // namespace fp4lin

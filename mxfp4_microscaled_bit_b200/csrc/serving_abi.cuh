@@ -65,15 +65,14 @@ cudaError_t launch_norm(const NormShape &a, int sms, cudaStream_t s)
 // Requests of at most KVP_SPLIT_ROWS (token, head) rows are the split kernel's, which streams the
 // cache at HBM speed; the others the tensor-core kernel's.  With 32 or 64 in its place, which makes the
 // split kernel read the cache once for every 16 rows (us for 16 / 32 / 64; 8 kv heads, D = 128):
-// 32 requests of 32 rows over 4096 keys 163 / 234 / 234, 64 of 20 rows 319 / 433 / 433, one of 32 rows
-// over 32768 keys 53 / 81 / 81, 16 of 32 rows over 600 keys 22 / 58 / 58; only one of 32 rows over
-// 2048 keys is better off there, 24 / 15 / 15.
+// 32 requests of 32 rows over 4096 keys 168 / 234 / 234, 64 of 20 rows 322 / 433 / 433, one of 32 rows
+// over 32768 keys 52 / 81 / 81, 16 of 32 rows over 600 keys 29 / 58 / 58; only one of 32 rows over
+// 2048 keys is better off there, 25 / 15 / 15.
 constexpr int KVP_SPLIT_ROWS = 16;
 
 struct KvPagedPlan {
     int nt, rows, tiles, chunk, S, max_rows;
-    int prefill_tiles;  // 0: no request can have more than KVP_SPLIT_ROWS rows
-    int prefill_chunk, prefill_S;
+    int64_t prefill_tiles;  // 0: no request can have more than KVP_SPLIT_ROWS rows
     size_t split_bytes, ws_bytes;  // the split kernel's share, and all
 };
 
@@ -85,36 +84,31 @@ KvPagedPlan plan_paged(int B, int H, int G, int max_new, int64_t max_len, int D,
     KvPagedPlan p{};
     const int64_t all = (int64_t)max_new * G, most = std::min<int64_t>(all, KVP_SPLIT_ROWS);
     p.max_rows = KVP_SPLIT_ROWS;
-    p.prefill_tiles = all > KVP_SPLIT_ROWS ? (int)((all + KPP_ROWS - 1) / KPP_ROWS) : 0;
-    p.nt = most <= 8 ? 1 : 2;
+    p.prefill_tiles = all > KVP_SPLIT_ROWS ? (all + KPP_ROWS - 1) / KPP_ROWS * B * H : 0;
+    // 8 rows a tile where none has more.  Next to longer requests the split kernel sees single tokens mostly,
+    // of G rows: 63 of 1000 keys, 8 heads of 4, beside a prompt take 64 us so, 145 in tiles of 16.
+    p.nt = (p.prefill_tiles ? G : most) <= 8 ? 1 : 2;
     p.rows = 8 * p.nt;
     p.tiles = (int)((most + p.rows - 1) / p.rows);
     const int64_t units = (int64_t)B * H * p.tiles;
     int64_t chunk = (max_len * units + (int64_t)sms * 12 - 1) / ((int64_t)sms * 12);
     chunk = (chunk + 127) / 128 * 128;
     chunk = std::min<int64_t>(std::max<int64_t>(chunk, 128), KVP_MAX_CHUNK);
-    // a second launch costs more than a second step of the warps
+    // a cluster joins up to 8 splits at once: longer splits are better than a second launch.  One request, 8
+    // heads, D = 128: 2000 keys 8.1 us, with a second launch 11.9; 3900 keys 10.3 and 15.8; 16000 keys 24
+    // and 51; the other way round are 16 requests of 3900 keys, 42.5 and 39.5.
     const int64_t joined = (max_len + 8 * 128 - 1) / (8 * 128) * 128;
-    if (chunk < joined && joined <= 256)
-        chunk = joined;
+    if (joined <= KVP_MAX_CHUNK)
+        chunk = std::max(chunk, joined);
+    else  // 1 / 4 requests of 32768 keys: from 256 / 512 / 1024 / 2048 on 28 / 26 / 20 / 27 and 62 / 63 / 63 / 69 us
+        chunk = std::max<int64_t>(chunk, 1024);
     p.chunk = (int)chunk;
     p.S = (int)((max_len + chunk - 1) / chunk);
     // up to 8 splits are one cluster, joined in the kernel; more leave their parts in the workspace
     p.split_bytes = p.S > 8 ? (size_t)units * p.S * p.rows * (D + 4) * sizeof(float) : 0;
     p.ws_bytes = p.split_bytes;
-    if (p.prefill_tiles) {
-        // a CTA an SM; with fewer tiles the keys are shared, at least 4 blocks to a CTA.  With at least
-        // 2 / 3 / 4 / 8 / 16 blocks, and unshared (8 kv heads, D = 128): one request of 32 rows over 8192
-        // keys 28 / 29 / 27 / 34 / 47 / 136 us, one of 512 rows over 4096 keys 38 / 34 / 36 / 43 / 61 / 91,
-        // one of 256 over 2048 27 / 30 / 31 / 40 / 55 / 54, one of 32 over 32768 51 / 53 / 51 / 51 / 54 / 512
-        const int64_t tiles = (int64_t)B * H * p.prefill_tiles, blocks = (max_len + KPP_KEYS - 1) / KPP_KEYS;
-        int64_t S = std::max<int64_t>(1, std::min(sms / tiles, blocks / 4));
-        const int64_t per = (blocks + S - 1) / S;
-        p.prefill_S = (int)((blocks + per - 1) / per);
-        p.prefill_chunk = (int)per * KPP_KEYS;
-        if (p.prefill_S > 1)
-            p.ws_bytes += (size_t)tiles * p.prefill_S * KPP_ROWS * (D + 4) * sizeof(float);
-    }
+    if (p.prefill_tiles)
+        p.ws_bytes += kpp_workspace(p.prefill_tiles, sms, D);
     return p;
 }
 
@@ -129,16 +123,16 @@ bool paged_sizes_ok(int B, int H, int G, int D, int max_new, int64_t max_len)
 template <int D>
 cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream_t s)
 {
-    if (p.prefill_tiles) {
-        cudaError_t e = launch_pdl(kv_paged_prefill_kernel<D>,
-                                   dim3((unsigned)p.prefill_tiles, (unsigned)(a.B * a.H), (unsigned)p.prefill_S),
-                                   dim3(KPP_THREADS), kpp_smem(D), s, a);
-        if (e == cudaSuccess && p.prefill_S > 1) {
-            const KvPagedParts parts{a.prefill_ws, KPP_ROWS, p.prefill_tiles, p.prefill_S, p.prefill_chunk, p.max_rows,
-                                     0x7FFFFFFF};
-            const dim3 mgrid((unsigned)(((int64_t)a.max_new * a.G + 3) / 4), (unsigned)(a.B * a.H));
-            e = launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a, parts);
-        }
+    if (a.prefill_most) {
+        cudaError_t e = launch_pdl(kv_paged_plan_kernel, dim3(1), dim3(KPP_PLAN_THREADS), 0, s, a);
+        if (e == cudaSuccess)
+            e = launch_pdl(kv_paged_prefill_kernel<D>, dim3((unsigned)kpp_grid(a.prefill_most, a.sms)), dim3(KPP_THREADS),
+                           kpp_smem(D), s, a);
+        if (e == cudaSuccess && a.max_len > KPP_MIN_BLOCKS * KPP_KEYS)  // else no tile is shared
+            e = launch_pdl(kv_paged_prefill_merge_kernel<D>,
+                           dim3(a.prefill_most * 9 <= a.sms ? KPP_ROWS : KPP_ROWS / KVP_WARPS,  // more than 8 parts, or not
+                                (unsigned)std::min(a.prefill_most, 2 * a.sms / 3)),
+                           dim3(KVP_THREADS), 0, s, a);
         if (e != cudaSuccess)
             return e;
     }
@@ -158,9 +152,8 @@ cudaError_t launch_paged(const KvPagedShape &a, const KvPagedPlan &p, cudaStream
                                     : cudaLaunchKernelEx(&cfg, kv_paged_split_kernel<D, 2>, a);
     if (e != cudaSuccess || p.S <= 8)
         return e;
-    const dim3 mgrid((unsigned)((std::min<int64_t>((int64_t)a.max_new * a.G, p.max_rows) + 3) / 4), (unsigned)(a.B * a.H));
-    return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(128), 0, s, a,
-                      KvPagedParts{a.ws, p.rows, p.tiles, p.S, p.chunk, 0, p.max_rows});
+    const dim3 mgrid((unsigned)std::min<int64_t>((int64_t)a.max_new * a.G, p.max_rows), (unsigned)(a.B * a.H));
+    return launch_pdl(kv_paged_merge_kernel<D>, mgrid, dim3(KVP_THREADS), 0, s, a, p.rows);
 }
 
 // ------------------------------------------------------------------ matvec
@@ -485,10 +478,14 @@ int kv_fp8_attention(const void *q, int64_t ld_q, int T, const uint8_t *k_codes,
     a.tiles = p.tiles;
     a.max_rows = p.max_rows;
     a.joined = p.S > 1 && p.S <= 8;
-    a.prefill_ws = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + p.split_bytes);
-    a.prefill_chunk = p.prefill_chunk;
-    a.prefill_S = p.prefill_S;
-    if (p.prefill_tiles) {
+    a.sms = dev->sms;
+    a.prefill_ws = reinterpret_cast<int4 *>(reinterpret_cast<uint8_t *>(workspace) + p.split_bytes);
+    if (p.prefill_tiles)
+        a.prefill_jobs = reinterpret_cast<KppJob *>(a.prefill_ws + kpp_jobs_at(p.prefill_tiles, dev->sms, D));
+    // no more tiles than T tokens can make: rows / 256, and a started one for each request of many rows
+    const int64_t q_rows = (int64_t)T * G, many = std::min<int64_t>(B, q_rows / (KVP_SPLIT_ROWS + 1));
+    a.prefill_most = (int)std::min(p.prefill_tiles, (q_rows / KPP_ROWS + many) * H);
+    if (a.prefill_most) {
         int ordinal = 0;
         if (cudaGetDevice(&ordinal) != cudaSuccess)
             return FP4LIN_ERR_CUDA;

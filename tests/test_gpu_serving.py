@@ -502,6 +502,30 @@ def test_attention_many_rows_with_the_keys_split(B, H, G, D, P, lens, new, max_l
     status_ok()
 
 
+def test_attention_prompts_among_many_decoding_requests():
+    """More than a thread's one request in the plan; tiles alone and, at the end, shared."""
+    lens, new = np.full(1500, 3), np.ones(1500, int)
+    lens[7::100] = 40
+    new[[3, 700, 701, 1499]] = [130, 70, 0, 300]
+    lens[[700, 1499]] = 600, 900
+    attention_check(*attention_case(1500, 1, 2, 64, 16, lens, new, seed=3), 16)
+    status_ok()
+    # more tiles than SMs, ends of requests inside a tile
+    attention_check(*attention_case(3, 10, 16, 64, 64, [30, 600, 5], [83, 90, 81], seed=4), 64)
+    status_ok()
+
+
+def test_attention_offsets_that_fall_and_rise_with_long_requests():
+    """Overlapping requests, which no plan has room for: reported, and nothing but rows of q's is written."""
+    q, caches, table, lens, cu = attention_case(9, 1, 4, 64, 16, [700] * 9, [60] * 9, seed=5)
+    (kc, kb), (vc, vb) = caches
+    cu = np.array([0, 60, 0, 60, 0, 60, 0, 60, 0, 60])
+    room = torch.full((80, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    fl.kv_fp8_attention(q[:60].to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu), max_new=60,
+                        max_len=760, out=room[:60])
+    assert fl.device_status() == OUT_OF_RANGE and (room[60:] == 7).all()
+
+
 def test_attention_nan_values_and_missing_pages_where_the_keys_are_split():
     q, caches, table, lens, cu = attention_case(1, 1, 8, 64, 16, [4000], [60], seed=4)
     (kc, kb), (vc, vb) = caches
@@ -591,7 +615,10 @@ def test_attention_refusals():
     with pytest.raises(fl.Fp4LinError, match="INVALID"):
         fl.kv_fp8_attention(*a, max_new=1, max_len=table.shape[1] * 16 + 1)
     with pytest.raises(fl.Fp4LinError, match="WORKSPACE"):
-        fl.kv_fp8_attention(*a, max_new=1, max_len=3001, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+        wide = gpu(np.pad(table, ((0, 0), (0, 1400)), constant_values=-1))  # more than a cluster's splits
+        fl.kv_fp8_attention(*a[:3], wide, *a[4:], max_new=1, max_len=20000, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(fl.Fp4LinError, match="WORKSPACE"):  # many rows, whose keys may be shared
+        fl.kv_fp8_attention(*a, max_new=20, max_len=3001, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="a multiple of 2 heads"):
         fl.kv_fp8_attention(a[0][:, :3], *a[1:], max_new=1, max_len=3001)
     with pytest.raises(TypeError, match="pair"):
