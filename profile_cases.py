@@ -11,7 +11,11 @@ kv_load (8 x 8 x 32768 x 128 cache to FP8; --kv-batch sets the 8 sequences), kv_
 attention over the same 8 x 8 caches, G = 4), quant_mse (the 14336 x 4096 weight,
 MSE-optimal scales), gemm_quant (the prefill GEMM with its output NVFP4-encoded),
 linear_decode (16 x 14336 x 4096 with the activation quantiser inside the GEMM),
-gptq (MR-GPTQ of the 14336 x 4096 weight, NVFP4, 16-wide rotation).
+gptq (MR-GPTQ of the 14336 x 4096 weight, NVFP4, 16-wide rotation), norm_mxfp8
+(8192 x 4096 with residual and 32-wide rotation), matvec_nvfp4 (5 x 4096 x 14336,
+bf16), matvec_mxfp4 (16 x 14336 x 4096, 8-bit activations), paged_store (8 prompts
+of 2048 tokens, 8 heads of 128), paged_decode (16 sequences of 32768 tokens, 8 kv
+heads, G = 4), paged_prefill (2 x 2048 new tokens behind 8192).
 """
 from __future__ import annotations
 
@@ -33,7 +37,8 @@ def main():
     ap.add_argument("--case", required=True,
                     choices=["gemm_prefill", "gemm_mxfp4", "gemm_decode", "quant_prefill", "quant_prefill_static",
                              "quant_prefill_static_h0", "kv_load", "kv_store", "kv_attention", "quant_mse",
-                             "gemm_quant", "linear_decode", "gptq"])
+                             "gemm_quant", "linear_decode", "gptq", "norm_mxfp8", "matvec_nvfp4", "matvec_mxfp4",
+                             "paged_store", "paged_decode", "paged_prefill"])
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--kv-batch", type=int, default=8,
                     help="sequences in the kv_* cases' cache (8 x 8 x 32768 x 128 by default)")
@@ -49,6 +54,35 @@ def main():
         u = fl.gptq_hessian_factor(torch.from_numpy(si.gptq_calibration(7, 2 * K, K)).to(dev), 16)
         ws = torch.empty(int(fl.lib().gptq_workspace_bytes(W.shape[0], K)), dtype=torch.uint8, device=dev)
         fn = lambda: fl.gptq_quantize(W, u, "nvfp4", 16, workspace=ws)  # noqa: E731
+    elif a.case == "norm_mxfp8":
+        x, r = si.prefill_A().to(dev), si.prefill_A().to(dev).flip(0).contiguous()
+        w = si.normal_bf16(3, 1, x.shape[1]).view(-1).to(dev)
+        fn = lambda: fl.rmsnorm_mxfp8(x, w, r, hadamard=32)  # noqa: E731
+    elif a.case.startswith("matvec"):
+        M, N, K = (5, 4096, 14336) if a.case == "matvec_nvfp4" else (16, 14336, 4096)
+        w = fl.prepare_weight(si.decode_W(N, K).to(dev), a.case[7:], 0)
+        x = si.decode_A(M, K).to(dev)
+        xs = None
+        if a.case == "matvec_mxfp4":
+            x, xs = fl.rmsnorm_mxfp8(x, torch.ones(K, dtype=torch.bfloat16, device=dev))[:2]
+        fn = lambda: fl.weight_only_linear(x, w, x_scales=xs)  # noqa: E731
+    elif a.case.startswith("paged"):
+        H, G, D, P = 8, 4, 128, 64
+        B, past, new = {"paged_store": (8, 0, 2048), "paged_decode": (16, 32767, 1), "paged_prefill": (2, 8192, 2048)}[a.case]
+        width = -(-(past + new) // P)
+        table = torch.randperm(B * width, device=dev).to(torch.int32).view(B, width)
+        caches = [(torch.randint(0, 126, (B * width, H, P, D), dtype=torch.uint8, device=dev),
+                   torch.full((B * width, H), 119, dtype=torch.uint8, device=dev)) for _ in range(2)]
+        lens = torch.full((B,), past, dtype=torch.int32, device=dev)
+        cu = (torch.arange(B + 1, device=dev) * new).to(torch.int32)
+        p = past + torch.arange(new, device=dev)
+        slots = (table[:, p // P] * P + p % P).to(torch.int32).view(-1)
+        kv = si.normal_bf16(7, B * new, H * D).to(dev).view(B * new, H, D)
+        q = si.normal_bf16(8, B * new, H * G * D).to(dev).view(B * new, H * G, D)
+        if a.case == "paged_store":
+            fn = lambda: fl.kv_fp8_store(kv, kv, slots, *caches)  # noqa: E731
+        else:
+            fn = lambda: fl.kv_fp8_attention(q, *caches, table, lens, cu, max_new=new, max_len=past + new)  # noqa: E731
     elif a.case == "linear_decode":
         M, N, K = 16, 14336, 4096
         w = fl.prepare_weight(si.decode_W(N, K).to(dev), "nvfp4", 0)
