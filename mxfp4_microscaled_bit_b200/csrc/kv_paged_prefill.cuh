@@ -30,6 +30,7 @@
 // kv_paged_prefill_merge_kernel: one request of 32 rows over 32768 keys takes 51 us instead of 512.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kv_paged_attention.cuh"
@@ -70,10 +71,11 @@ __host__ __device__ inline KppSplit kpp_split(int alive, int sms)
     return {sms / 4, 4};
 }
 
-// The most CTAs that up to `most` tiles can become, and of them those that share a tile.
+// The most CTAs that up to `most` tiles can become, and of them those that share a tile.  Neither falls as
+// `most` grows: a call's tokens may allow fewer tiles than its workspace was sized for.
 inline int64_t kpp_grid(int64_t most, int sms)
 {
-    return most <= sms / 2 ? sms : most <= sms ? 2 * sms : most + 3 * (sms / 4);
+    return most <= sms / 2 ? sms : std::max<int64_t>(2 * sms, most + 3 * (sms / 4));
 }
 inline int64_t kpp_parts(int64_t most, int sms) { return most <= sms / 2 ? sms : 2 * (int64_t)sms; }
 

@@ -515,6 +515,19 @@ def test_attention_prompts_among_many_decoding_requests():
     status_ok()
 
 
+def test_attention_few_long_requests_where_the_batch_allows_more():
+    """98 requests of many rows, three CTAs each, in a batch that might have had 150."""
+    lens, new = np.full(150, 1600), np.ones(150, int)
+    new[:98] = 26
+    q, caches, table, lens, cu = attention_case(150, 1, 1, 64, 128, lens, new, seed=6)
+    attention_check(q, caches, table, lens, cu, 128)
+    # fewer than its workspace has room for: 140 requests of q's length
+    n = np.where(np.arange(150) < 90, 26, 0)
+    cu = np.concatenate([[0], np.cumsum(n)])
+    attention_check(q[:cu[-1]], caches, table, lens, cu, 128)
+    status_ok()
+
+
 def test_attention_offsets_that_fall_and_rise_with_long_requests():
     """Overlapping requests, which no plan has room for: reported, and nothing but rows of q's is written."""
     q, caches, table, lens, cu = attention_case(9, 1, 4, 64, 16, [700] * 9, [60] * 9, seed=5)
