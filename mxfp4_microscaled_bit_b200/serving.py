@@ -107,18 +107,19 @@ def _device(fn: str, name: str, t) -> int:
     raise ValueError(f"{fn}: {name} must be a CUDA tensor, not on {t.device}")
 
 
-def _raw_stream(stream, dev: int) -> int:
+def _raw_stream(stream, dev: int, made=()) -> int:
+    """The stream's handle.  made: tensors that this call took from the current stream's memory.  Another
+    stream first waits for what that memory may still serve, and it is not given out again before that
+    stream is done with it."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)  # current_stream() without making a Stream object
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _hand_over(stream, dev: int, tensors) -> None:
-    """Tensors made here on the current stream and used on `stream`: their memory is not given out
-    again before that stream is done with it."""
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
-    for t in tensors:
-        t.record_stream(s)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if made and raw != torch._C._cuda_getCurrentRawStream(dev):
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(raw, device=dev)
+        s.wait_stream(torch.cuda.current_stream(dev))
+        for t in made:
+            t.record_stream(s)
+    return raw
 
 
 def _scale_bytes(rows: int, cols: int) -> int:
@@ -176,11 +177,9 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     else:
         _arg(fn, "scales", scales, _U8, need, dev)
     st = _lib().rmsnorm_mxfp8(x.data_ptr(), ld_x, r, ld_r, w, eps, hadamard, rows, cols, codes.data_ptr(),
-                              scales.data_ptr(), s, ld_s, _raw_stream(stream, dev))
+                              scales.data_ptr(), s, ld_s, _raw_stream(stream, dev, made))
     if st:
         _fail(fn, st)
-    if stream is not None:
-        _hand_over(stream, dev, made)
     return codes, scales, x if residual is None else summed
 
 
@@ -200,21 +199,20 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
     w = _arg(fn, "w_codes", w_codes, _U8, 0, dev)
     ws = _arg(fn, "w_scales", w_scales, _U8, _scale_bytes(N, K // (16 if nv else 32)), dev)
     ldy = N
-    made = out is None
-    if made:
+    made = ()
+    if out is None:
         out = _empty_strided((M, N), (N, 1), _BF16)
+        made = (out,)
     else:
         ldy = _rows(fn, "out", out, _BF16, (M, N), N, dev)
     if nv:
         st = _lib().nvfp4_matvec(x.data_ptr(), xs, M, K, ld_x, hadamard, w, ws, _arg(fn, "g_w", g_w, _F32, 1, dev),
-                                 out.data_ptr(), N, ldy, _raw_stream(stream, dev))
+                                 out.data_ptr(), N, ldy, _raw_stream(stream, dev, made))
     else:
         st = _lib().mxfp4_matvec(x.data_ptr(), xs, M, K, ld_x, hadamard, w, ws, out.data_ptr(), N, ldy,
-                                 _raw_stream(stream, dev))
+                                 _raw_stream(stream, dev, made))
     if st:
         _fail(fn, st)
-    if made and stream is not None:
-        _hand_over(stream, dev, (out,))
     return out
 
 
@@ -279,11 +277,9 @@ def kv_block_tables(block_table, lens, new_lens, free_pages, free_head, page: in
         _arg(fn, "next_head", next_head, _I32, 1, dev)
     st = _lib().kv_block_tables(block_table.data_ptr(), ld, width, pl, pn, B, pf, free_pages.numel(), ph, page,
                                 max_tokens, cu_new.data_ptr(), slots.data_ptr(), next_head.data_ptr(),
-                                _raw_stream(stream, dev))
+                                _raw_stream(stream, dev, made))
     if st:
         _fail(fn, st)
-    if stream is not None:
-        _hand_over(stream, dev, made)
     return cu_new, slots, next_head
 
 
@@ -367,9 +363,7 @@ def kv_fp8_attention(q, k_cache, v_cache, block_table, lens, cu_new, *, max_new:
         pw, need = _arg(fn, "workspace", workspace, getattr(workspace, "dtype", None), 0, dev), workspace.numel() * workspace.element_size()
     st = L.kv_fp8_attention(q.data_ptr(), ld_q, T, kc, ks, vc, vs, NP, P, block_table.data_ptr(), ld_t, width, pl, pcu,
                             max_new, max_len, D ** -0.5 if scale is None else scale, out.data_ptr(), B, H, G, D, pw,
-                            need, _raw_stream(stream, dev))
+                            need, _raw_stream(stream, dev, made))
     if st:
         _fail(fn, st)
-    if stream is not None:
-        _hand_over(stream, dev, made)
     return out

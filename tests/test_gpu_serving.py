@@ -709,6 +709,26 @@ def test_serving_steps_against_the_plain_forms():
         st.advance(n, head)
 
 
+def test_memory_made_for_another_stream_is_not_taken_from_pending_work():
+    """Memory that the current stream has freed but not finished with is given to no call on another."""
+    q, caches, table, lens, cu = attention_case(2, 1, 4, 64, 32, [300, 100], [40, 30], seed=1)
+    a = [q.to(DEV), *[(u8(c), u8(b)) for c, b in caches], gpu(table), gpu(lens), gpu(cu)]
+    want = fl.kv_fp8_attention(*a, max_new=40, max_len=340).clone()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(3):
+        held = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device=DEV)
+        seen = torch.empty_like(held)
+        torch.cuda._sleep(20_000_000)
+        seen.copy_(held)
+        del held
+        out = fl.kv_fp8_attention(*a, max_new=40, max_len=340, stream=other)
+        torch.cuda.synchronize()
+        assert (seen == 3).all() and torch.equal(out[:70], want[:70])
+        del out, seen
+    status_ok()
+
+
 def test_serving_step_captured_replayed_and_on_another_stream():
     runs = []
     for mode in ("eager", "graph", "stream"):
