@@ -19,8 +19,9 @@
 // CTAs that share rows form a cluster (at most 8) along K.  The partial sums of a row go to one CTA of
 // the cluster through distributed shared memory and are added in a fixed order: one launch, no
 // workspace, the same bits every time.  Between launches of a graph: NVFP4, one rotated row, 4096 x 4096
-// 5.1 us; five rows, 4096 x 14336 13.0 us (2.5 TB/s); MXFP4, sixteen 8-bit rows, 14336 x 4096 22.6 us, where
-// the eight warps of a CTA each turn the same x fragments and the CTAs do not fill the SMs evenly.
+// 5.1 us; five rows, 4096 x 14336 12.2 us (2.7 TB/s); MXFP4, sixteen 8-bit rows, 14336 x 4096 17.8 us, of which
+// ~9 us are the weights' loads alone (two chunks of each warp in flight), the rest the conversions, scales
+// and products of 16 warps an SM.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -52,11 +53,17 @@ struct MatvecShape {
     bool wide_w;
 };
 
+// Rows of x from one word of a lane's 64 values to the next in shared memory.  Odd, and lane slot t of word
+// i sits at t ^ (i / 2): eight lanes that write one row's words, or read eight rows' word, meet each bank
+// once (with a stride of 16 and no exchange the writes took 32 cycles a warp, and 16 rows of 14336 x 4096
+// MXFP4 weights 20.2 us instead of 17.8).
+__host__ __device__ constexpr int mv_stride(int M) { return M | 1; }
+
 // Shared memory: a segment's x as B fragments (16 bytes for 8 consecutive k of one row) with the
 // scale of each (chunk, row), and the partial sums that the cluster's warps send this CTA.
 constexpr size_t mv_smem(int M, int chunks, int ranks)
 {
-    return (size_t)chunks * MV_CHUNK * M * 2 + MV_SEG * MV_MAX_M * 4 + (size_t)ranks * M * ((MV_ROWS + ranks - 1) / ranks) * 4;
+    return (size_t)chunks * MV_CHUNK * mv_stride(M) * 2 + MV_SEG * MV_MAX_M * 4 + (size_t)ranks * M * ((MV_ROWS + ranks - 1) / ranks) * 4;
 }
 
 // A lane's share of a (row, chunk) of x: 8 consecutive values, raw.
@@ -181,9 +188,9 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
     const int tile = blockIdx.x / ranks;
     const SmallDiv by_ranks(ranks);
     const int c0 = rank * a.per_cta, c1 = min(c0 + a.per_cta, a.nchunks);
-    const int seg_chunks = min(a.per_cta, MV_SEG);
+    const int seg_chunks = min(a.per_cta, MV_SEG), ms = mv_stride(a.M);
     uint4 *s_x = reinterpret_cast<uint4 *>(mv_dyn);
-    float *s_xs = reinterpret_cast<float *>(mv_dyn + (size_t)seg_chunks * MV_CHUNK * a.M * 2);  // [chunk][MV_MAX_M]
+    float *s_xs = reinterpret_cast<float *>(mv_dyn + (size_t)seg_chunks * MV_CHUNK * ms * 2);  // [chunk][MV_MAX_M]
     float *s_y = s_xs + MV_SEG * MV_MAX_M;           // [source rank][M][rows of this rank]
     const int own = (MV_ROWS + ranks - 1) / ranks;  // the CTA's row n is rank n % ranks'
 
@@ -245,7 +252,8 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
         __syncthreads();  // the last segment's fragments are done with
 #pragma unroll 1
         for (int m = xm; m < a.M; m += 8) {
-            uint4 *to = s_x + ((lane & 7) * a.M + m) * 4 + (lane >> 3);  // word lane % 8 of lane slot t = lane / 8
+            // word i = lane % 8 of lane slot t = lane / 8
+            uint4 *to = s_x + ((lane & 7) * ms + m) * 4 + ((lane >> 3) ^ ((lane & 7) >> 1));
 #pragma unroll 1
             for (int c = xc; c < chunks; c += BATCH * xstep) {
                 if (m != xm || c != xc)
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                     if (cb < chunks) {
                         uint4 f;
                         const float scale = mv_stage<X8, HAD>(raw[b], lane, f);
-                        to[cb * 32 * a.M] = f;
+                        to[cb * 32 * ms] = f;
                         if (lane == 0)
                             s_xs[cb * MV_MAX_M + m] = scale;
                     }
@@ -298,16 +306,16 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                 fA = mxfp8_scale(refA);
                 fB = mxfp8_scale(refB);
             }
-            // several sums side by side: an MMA that waits for the last one's takes four times as long
-            constexpr int CHAINS = NT == 1 ? 4 : 2;
+            // two sums side by side (four: 5% slower, the warps of an SM hide an MMA's latency already)
+            constexpr int CHAINS = 2 / NT;
             float acc[CHAINS][NT][4];
 #pragma unroll
             for (int q = 0; q < CHAINS; ++q)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     acc[q][nt][0] = acc[q][nt][1] = acc[q][nt][2] = acc[q][nt][3] = 0.0f;
-            const uint4 *xc = s_x + (c - sb) * 32 * a.M + t;
-            const int step = 4 * a.M;
+            const uint4 *xc = s_x + (c - sb) * 32 * ms;
+            const int step = 4 * ms;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint32_t ha[4], hb[4];
@@ -315,7 +323,7 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                 mv_weights(vb[i], sB[i >> 1], hb);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 f = xc[i * step + 4 * xrow[nt]];
+                    const uint4 f = xc[i * step + 4 * xrow[nt] + (t ^ (i >> 1))];
                     mma_16816x(acc[(2 * i) % CHAINS][nt], ha[0], hb[0], ha[1], hb[1], f.x, f.y);
                     mma_16816x(acc[(2 * i + 1) % CHAINS][nt], ha[2], hb[2], ha[3], hb[3], f.z, f.w);
                 }
@@ -324,9 +332,9 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {  // columns 2t, 2t+1 of the token tile; rows A, A, B, B
-                    float sum = acc[0][nt][e] + acc[1][nt][e];
-                    if constexpr (CHAINS == 4)
-                        sum += acc[2][nt][e] + acc[3][nt][e];
+                    float sum = acc[0][nt][e];
+                    if constexpr (CHAINS == 2)
+                        sum += acc[1][nt][e];
                     const float xs = s_xs[(c - sb) * MV_MAX_M + 8 * nt + 2 * t + (e & 1)];
                     tot[nt][e] = NV ? fmaf(sum, xs, tot[nt][e]) : fmaf(sum * xs, e < 2 ? fA : fB, tot[nt][e]);
                 }

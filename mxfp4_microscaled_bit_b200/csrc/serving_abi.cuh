@@ -65,8 +65,8 @@ cudaError_t launch_norm(const NormShape &a, int sms, cudaStream_t s)
 // Requests of at most KVP_SPLIT_ROWS (token, head) rows are the split kernel's, which streams the
 // cache at HBM speed; the others the tensor-core kernel's.  With 32 or 64 in its place, which makes the
 // split kernel read the cache once for every 16 rows (us for 16 / 32 / 64; 8 kv heads, D = 128):
-// 32 requests of 32 rows over 4096 keys 168 / 234 / 234, 64 of 20 rows 322 / 433 / 433, one of 32 rows
-// over 32768 keys 52 / 81 / 81, 16 of 32 rows over 600 keys 29 / 58 / 58; only one of 32 rows over
+// 32 requests of 32 rows over 4096 keys 158 / 234 / 234, 64 of 20 rows 303 / 433 / 433, one of 32 rows
+// over 32768 keys 51 / 81 / 81, 16 of 32 rows over 600 keys 28 / 58 / 58; only one of 32 rows over
 // 2048 keys is better off there, 25 / 15 / 15.
 constexpr int KVP_SPLIT_ROWS = 16;
 
