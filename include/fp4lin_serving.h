@@ -142,7 +142,8 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
  *   lens + n <= max_len <= width * P for every request.  A request that breaks
  *   this (or has negative lengths or rows behind T) is skipped, a page outside
  *   [0, num_pages) counts as not visible; both are recorded as
- *   FP4LIN_ERR_OUT_OF_RANGE.
+ *   FP4LIN_ERR_OUT_OF_RANGE.  Where cu_new falls anywhere, other requests may be
+ *   skipped too.
  * D = 64 or 128; 1 <= G <= 16; B * H <= 65535; max_new * G <= 524280; scale
  * bytes as kv_fp8_store writes them (at most 253).  Rows of the cache behind a
  * request's last may hold anything.  Scores, softmax and sums are binary32, the
