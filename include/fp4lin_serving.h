@@ -146,8 +146,10 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
  *   skipped too.
  * D = 64 or 128; 1 <= G <= 16; B * H <= 65535; max_new * G <= 524280; scale
  * bytes as kv_fp8_store writes them (at most 253).  Rows of the cache behind a
- * request's last may hold anything.  Scores, softmax and sums are binary32, the
- * softmax weights rounded to f16.  workspace: at least
+ * request's last may hold anything.  Scores, softmax and sums are binary32.  The
+ * softmax weights, each times its page's value scale, are rounded to f16: within
+ * 2^-11 of themselves, or 2^-39 of the row's largest (2^-31 where a request has
+ * more than 16 (token, head) rows).  workspace: at least
  * kv_fp8_attention_workspace_bytes bytes for the same sizes (may be 0, then
  * NULL will do), 16-byte aligned, of this call alone.
  */

@@ -11,8 +11,13 @@
 // scales.  A page whose value byte is 0 (all codes zero) takes part in the second sum only; it uses
 // the exponent of KVP_ZERO_X there, so that it does not move M far.
 // Scores, maxima, sums and outputs are binary32.  K and V codes are exact in f16; q is scaled by a
-// power of two to [1, 2) at its row's maximum (exact down to 2^-14 of it); the weights are rounded
-// to f16 (2^-11 each, against bf16 outputs).
+// power of two to [1, 2) at its row's maximum (exact down to 2^-14 of it).  The weights that meet
+// the value codes are rounded to f16: to 2^-11 of themselves against bf16 outputs, and below f16's
+// normals to half its smallest step, 2^-25.  So they are kept high in f16, at most 2^KVP_BIAS and a
+// binade or two above where scores pass 2^23: M is held that far below the maximum, and the split kernel
+// loses only what is 2^-39 of a row's largest (2^-25 with the largest at 1, where all keys beside one of
+// 18 more were lost).  The second sum leaves the factor out, with its 2^-Xv, so that values of any
+// magnitude keep their room in binary32; the first leaves it out at its end.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -28,6 +33,10 @@ constexpr int KVP_WARPS = KVP_THREADS / 32;
 constexpr int KVP_MAX_CHUNK = 2048;    // keys a CTA
 constexpr int KVP_STEP = 32;           // keys a warp takes at a time
 constexpr float KVP_ZERO_X = -8.0f;
+constexpr int KVP_BIAS = 14;           // log2 of the largest weight
+
+// 2^k for a constant k.
+__host__ __device__ constexpr float pow2_const(int k) { return k < 0 ? 0.5f * pow2_const(k + 1) : k ? 2.0f * pow2_const(k - 1) : 1.0f; }
 
 struct KppJob;
 
@@ -71,6 +80,14 @@ __device__ __forceinline__ float ex2(float x)
 {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// f16x2 of two weights; one that passes f16 (from 2^14 by the scores' own rounding) stays finite.
+__device__ __forceinline__ uint32_t cvt_f16x2_finite(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
@@ -274,7 +291,7 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
             const bool in = kb + 16 * u < k1;
             const float kf = in ? s_kf[i] : 0.0f;
             xv[u] = in ? s_xv[i] : -INFINITY;
-            c[u] = ex2(-xv[u]);
+            c[u] = ex2(-xv[u]) * pow2_const(-KVP_BIAS);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                m = fmaxf(m, M[nt][e]);
+                m = fmaxf(m - KVP_BIAS, M[nt][e]);
                 const float base = m == -INFINITY ? 0.0f : m;
                 corr[e] = ex2(M[nt][e] - base);
                 M[nt][e] = m;
@@ -326,8 +343,8 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                wb[u][nt][0] = movmatrix(cvt_f16x2(s[u][nt][0], s[u][nt][1]));
-                wb[u][nt][1] = movmatrix(cvt_f16x2(s[u][nt][2], s[u][nt][3]));
+                wb[u][nt][0] = movmatrix(cvt_f16x2_finite(s[u][nt][0], s[u][nt][1]));
+                wb[u][nt][1] = movmatrix(cvt_f16x2_finite(s[u][nt][2], s[u][nt][3]));
             }
         }
         if (kb + KVP_STEP - 1 > rq.len + imin) {
@@ -408,7 +425,7 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
             sum = fmaf(f, s_den[w][r], sum);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j] = fmaf(f, s_o[w][r][d + j], v[j]);
+                v[j] = fmaf(f * pow2_const(-KVP_BIAS), s_o[w][r][d + j], v[j]);
         }
         if (any_nan) {
             const int last = min(k1 - 1, rq.len + (row0 + r) / a.G);

@@ -12,8 +12,8 @@
 //                    applies both scales in one multiply-add, writes the f16 weights over the scores
 //                    in TMEM; meanwhile the next 64 are computed into the tile's other buffer (with
 //                    one buffer of 128 the kernel took 799 us).  The output is rescaled only when the
-//                    maximum has grown by more than 2^8 (the weights stay below 2^8, far inside f16),
-//                    which is rare.
+//                    maximum has grown by more than 2^KPP_LAZY, which is rare; the weights start at
+//                    2^KPP_BIAS, so that they stay in f16 and lose only what is 2^-31 of a row's largest.
 //   warps 8-11       load 128 keys of K and V from their pages, a block ahead in registers, and
 //                    write them as f16 (exact) in the 128-byte-swizzled operand layout.
 //   warp 13          waits for what warp 12 needs next and meets it at a named barrier, which costs the
@@ -43,7 +43,8 @@ constexpr int KPP_ROWS = 256;          // rows a CTA
 constexpr int KPP_SLOTS = 4;           // blocks whose page factors are held at once
 constexpr int KPP_MIN_BLOCKS = 4;      // blocks of keys to a CTA, at least (one request of 512 rows over 4096
                                        // keys: 2 / 3 / 4 / 8 / 16 take 38 / 34 / 36 / 43 / 61 us)
-constexpr float KPP_LAZY = 8.0f;       // log2 growth of the maximum that is let pass
+constexpr int KPP_LAZY = 8;            // log2 growth of the maximum that is let pass
+constexpr int KPP_BIAS = KVP_BIAS - KPP_LAZY;  // how far below the maximum M is put
 
 struct KppCtrl {
     uint64_t kfull[2], kfree[2], vfull[2], vfree[2], sfull[2][2], pfull[2][2], odone[2], drain;
@@ -450,9 +451,9 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     m = fmaxf(m, fmaf(fmaxf(t0, t1), f[g], x[g]));
                 }
                 float corr = 1.0f;
-                if (m > M + KPP_LAZY || (M == -INFINITY && m > M)) {
-                    corr = ex2(M - m);  // 0 for the first keys
-                    M = m;
+                if (m - M > (float)KVP_BIAS) {  // NaN while no key was seen
+                    corr = ex2(M - (m - KPP_BIAS));  // 0 for the first keys
+                    M = m - KPP_BIAS;
                 }
                 // The last product is waited for before the output is scaled, and always before the last
                 // weights are given out: the wait after the loop then has one phase only to mean.
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                             f2_unpack(f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), f2, x2), a0, a1);
                             const float w0 = ex2(a0), w1 = ex2(a1);
                             sum = f2_add(sum, f2_pack(w0, w1));
-                            w[8 * g + j / 2] = cvt_f16x2(w0, w1);
+                            w[8 * g + j / 2] = cvt_f16x2_finite(w0, w1);
                         }
                         float s0, s1;
                         f2_unpack(sum, s0, s1);
@@ -499,7 +500,9 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             if (ok && warp_wait(&ct.odone[tile], 1, abort, lane)) {
                 tc_fence_after();
                 const bool whole = job.sums < 0;
-                const float inv = !whole ? 1.0f : den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den;
+                // the sums without the bias: den has none, the products do
+                const float inv =
+                    pow2_const(-KPP_BIAS) * (!whole ? 1.0f : den > 0.0f ? __fdiv_rn(1.0f, den) : den == 0.0f ? 0.0f : den);
                 __nv_bfloat16 *dst =
                     a.out + (int64_t)(job.first + (mine ? tok : 0)) * a.H * a.G * D + (int64_t)(h * a.G + (mine ? head : 0)) * D;
                 float *sums = reinterpret_cast<float *>(a.prefill_ws + 1 + a.sms) +
@@ -522,7 +525,8 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                     } else if (mine) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(sums + 32 * k + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            *reinterpret_cast<float4 *>(sums + 32 * k + j) =
+                                make_float4(o[j] * inv, o[j + 1] * inv, o[j + 2] * inv, o[j + 3] * inv);
                     }
                 }
                 if (mine && !whole)
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                 const float x = vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X;
                 ct.kf[slot][lane] = mxfp8_scale(kbyte);
                 ct.xv[slot][lane] = page >= 0 ? x : -INFINITY;
-                ct.c[slot][lane] = page >= 0 ? ex2(-x) : 0.0f;
+                ct.c[slot][lane] = page >= 0 ? ex2(-x) * pow2_const(-KPP_BIAS) : 0.0f;
             }
             kbyte = next >= 0 ? a.ks[(int64_t)next * a.H + h] : 0u;
             vbyte = next >= 0 ? a.vs[(int64_t)next * a.H + h] : 0u;

@@ -1,0 +1,111 @@
+"""The serving operators where values lie far apart: dominant keys, pages of zeros, block scales and
+channels many binades from each other.  Plain 64-bit forms as in test_gpu_serving."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_microscaled_bit_b200 as fl
+import serving_ref as ref
+from gpu_util import DEV, status_ok
+from test_gpu_serving import BF16, F16, F32, attention_case, gpu, u8, within
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention
+def weight_floor(q, kc, kb, vc, vb, table, lens, cu, P, scale):
+    """The absolute part of the weights' f16 rounding.  A weight and its page's value scale make one
+    number W = p 2^Xv, held relative to the row's largest, which sits in f16 at 2^14 where a request has
+    up to 16 (token, head) rows and at 2^6 or above where it has more: half a step of a subnormal f16
+    is 2^-25, so every W is within 2^-39 (2^-31) of the largest, and meets |code|.  A page of zero
+    values (byte 0) has a part in the largest 2^-24 below the pages with values at most."""
+    T, HQ, D = q.shape
+    NP, H = kb.shape
+    G = HQ // H
+    floor = np.zeros((T, HQ, D))
+    for b in range(len(lens)):
+        n = cu[b + 1] - cu[b]
+        L = lens[b] + n
+        if n <= 0:
+            continue
+        part = 2.0 ** (-39 if n * G <= 16 else -31)
+        pages = table[b, :-(-L // P)]
+        for h in range(H):
+            k = ref.cache_values(kc[pages, h], kb[pages, h]).reshape(-1, D)[:L]
+            code = np.abs(ref.E4M3[vc[pages, h]]).reshape(-1, D)[:L]
+            x = np.repeat(vb[pages, h].astype(np.float64) - 127, P)[:L]
+            held = x > -127
+            for i in range(n):
+                see = np.arange(L) <= lens[b] + i
+                if not (see & held).any():
+                    continue
+                xs = np.where(held, x, x[see & held].max() - 24)
+                for j in range(h * G, (h + 1) * G):
+                    s = scale * (k[see] @ q[cu[b] + i, j])
+                    p = np.exp(s - s.max())
+                    W = p / p.sum() * 2.0 ** xs[see]
+                    floor[cu[b] + i, j] = part * W.max() * code[see].sum(0)
+    return floor
+
+
+def range_check(q, caches, table, lens, cu, P):
+    (kc, kb), (vc, vb) = caches
+    T, HQ, D = q.shape
+    n = np.diff(cu)
+    out = torch.full((T, HQ, D), 123.0, dtype=torch.bfloat16, device=DEV)
+    fl.kv_fp8_attention(q.to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)), gpu(table), gpu(lens), gpu(cu),
+                        max_new=int(n.max()), max_len=int((lens + n).max()), out=out)
+    status_ok()
+    a = ref.f64(q), kc, kb, vc, vb, table, lens, cu, P, D ** -0.5
+    want, spread, dots = ref.attention(*a)
+    mine = ~np.isnan(want)
+    got = ref.f64(out)
+    assert (got[~mine] == 123.0).all(), "rows of no request were written"
+    L = int((lens + n).max())
+    # a weight's relative error as in test_gpu_serving's attention_check, and the floor
+    tol = (2 * ((D + 6) * F32 * dots + 2.0 ** -21) + F16 + 2 * L * F32) * spread + weight_floor(*a)
+    within(got[mine], want[mine], (tol * (1 + BF16) + BF16 * np.abs(want))[mine], "attention")
+
+
+def sink(q, caches, table, P, G, D, row, gap, whole_page):
+    """Key `row` of request 0 with a logit about `gap` above every other's and a zero value; with
+    whole_page its page holds no other values either (byte 0)."""
+    (kc, kb), (vc, vb) = caches
+    H = kb.shape[1]
+    page, at = table[0, row // P], row % P
+    kc[:, :, :, 0] = 0
+    kc[page, :, at] = 0
+    kc[page, :, at, 0] = 0x7E
+    for h in range(H):
+        top = 448.0 * 2.0 ** (float(kb[page, h]) - 127)
+        q[:, h * G:(h + 1) * G, 0] = gap / (top * D ** -0.5)
+    vc[:] &= 0x7F  # values of one sign: what is lost does not average out
+    vc[page, :, at] = 0
+    if whole_page:
+        vc[page], vb[page] = 0, 0
+
+
+@pytest.mark.parametrize("whole_page", [False])
+@pytest.mark.parametrize("D,G,P,L,new,gap", [
+    (128, 4, 16, 4000, 1, 20.0),    # the split kernel, its splits joined in a cluster
+    (64, 4, 64, 20000, 1, 20.0),    # and through the workspace
+    (128, 8, 32, 1500, 2, 20.0),    # 16 rows
+    (64, 2, 16, 300, 40, 18.0),     # the many-row kernel, a tile's keys in one CTA
+    (128, 4, 64, 4000, 70, 18.0)])  # and shared among CTAs
+def test_attention_of_a_dominant_key_without_a_value(D, G, P, L, new, gap, whole_page):
+    q, caches, table, lens, cu = attention_case(1, 2, G, D, P, [L], [new], seed=L, sigma=0.4, spread=0.3)
+    sink(q, caches, table, P, G, D, 5, gap, whole_page)
+    range_check(q, caches, table, lens, cu, P)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("big", [2.0 ** 10, 2.0 ** 18, 2.0 ** 24])
+def test_attention_of_scores_whose_rounding_passes_the_weights_room(new, big):
+    """Scores so large that binary32 rounds them by whole binades: no weight becomes infinite, and
+    the answer stays among the values."""
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(1, 2, 4, 64, 32, [500], [new], seed=6)
+    out = fl.kv_fp8_attention((q.float() * big).to(torch.bfloat16).to(DEV), (u8(kc), u8(kb)), (u8(vc), u8(vb)),
+                              gpu(table), gpu(lens), gpu(cu), max_new=new, max_len=500 + new)[:new]
+    status_ok()
+    held = np.nan_to_num(np.abs(ref.cache_values(vc, vb))).max()
+    assert bool(out.isfinite().all()) and float(out.abs().max()) <= held * (1 + 2 * BF16)
