@@ -149,7 +149,9 @@ int kv_fp8_store(const void *k_new, int64_t ld_k, const void *v_new, int64_t ld_
  * request's last may hold anything.  Scores, softmax and sums are binary32.  The
  * softmax weights, each times its page's value scale, are rounded to f16: within
  * 2^-11 of themselves, or 2^-39 of the row's largest (2^-31 where a request has
- * more than 16 (token, head) rows).  workspace: at least
+ * more than 16 (token, head) rows).  Value scales of one request and head are
+ * taken to be within 2^64 of one another and at least 2^-80, pages of zeros
+ * (byte 0) apart.  workspace: at least
  * kv_fp8_attention_workspace_bytes bytes for the same sizes (may be 0, then
  * NULL will do), 16-byte aligned, of this call alone.
  */

@@ -8,8 +8,9 @@
 //   w_l = 2^(s'_l - M),  o = (sum_l w_l v_l) / (sum_l w_l 2^-Xv(l)),
 // so one running maximum and one exponential a score serve both sums, the weights that meet the
 // value codes are at most 1 whatever the pages' scales, and one fused multiply-add applies both
-// scales.  A page whose value byte is 0 (all codes zero) takes part in the second sum only; it uses
-// the exponent of KVP_ZERO_X there, so that it does not move M far.
+// scales.  A page whose value byte is 0 (all codes zero) takes part in the second sum only, under any
+// exponent.  Its keys should not move M, nor vanish beside it: it gets KVP_ZERO_GAP less than the least
+// of a CTA's other pages.  (A constant, -8, put M 2^29 above pages of values near 2^-37.)
 // Scores, maxima, sums and outputs are binary32.  K and V codes are exact in f16; q is scaled by a
 // power of two to [1, 2) at its row's maximum (exact down to 2^-14 of it).  The weights that meet
 // the value codes are rounded to f16: to 2^-11 of themselves against bf16 outputs, and below f16's
@@ -32,7 +33,8 @@ constexpr int KVP_THREADS = 128;
 constexpr int KVP_WARPS = KVP_THREADS / 32;
 constexpr int KVP_MAX_CHUNK = 2048;    // keys a CTA
 constexpr int KVP_STEP = 32;           // keys a warp takes at a time
-constexpr float KVP_ZERO_X = -8.0f;
+constexpr float KVP_ZERO_GAP = 24.0f;
+constexpr float KVP_ZERO_X = -8.0f;    // pages of zeros where there are no others
 constexpr int KVP_BIAS = 14;           // log2 of the largest weight
 
 // 2^k for a constant k.
@@ -74,6 +76,20 @@ __device__ __forceinline__ KvPagedRequest kvp_request(const KvPagedShape &a, int
            (int64_t)r.len + n <= a.max_len;
     r.n = r.ok ? (int)n : 0;
     return r;
+}
+
+// The exponent of a page of zeros beside others whose least is `low` (infinite: there are none).
+__device__ __forceinline__ float kvp_zero_exponent(float low)
+{
+    return low == INFINITY ? KVP_ZERO_X : fmaxf(low - KVP_ZERO_GAP, -126.0f);
+}
+
+__device__ __forceinline__ float warp_min(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = fminf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -256,14 +272,26 @@ __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_k
     int kb = k0 + warp * KVP_STEP;
     load_k(kb);
     load_v(kb);
+    bool zeros = false;
     for (int i = tid; i < groups; i += KVP_THREADS) {  // the scales, while the first rows are on their way
         const int page = s_page[i];
         const bool ok = page >= 0;
         const uint32_t kbyte = ok ? a.ks[(int64_t)page * a.H + h] : 0u, vbyte = ok ? a.vs[(int64_t)page * a.H + h] : 0u;
         s_kf[i] = mxfp8_scale(kbyte);
-        s_xv[i] = ok ? (vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X) : -INFINITY;  // no page: weight 0
+        // no page: weight 0; a page of zeros: infinite for now
+        s_xv[i] = ok ? (vbyte ? (float)((int)vbyte - 127) : INFINITY) : -INFINITY;
+        zeros |= ok && !vbyte;
     }
-    __syncthreads();
+    if (__syncthreads_or(zeros)) {
+        float low = INFINITY;
+        for (int i = lane; i < groups; i += 32)
+            low = fminf(low, s_xv[i] == -INFINITY ? INFINITY : s_xv[i]);
+        low = kvp_zero_exponent(warp_min(low));
+        __syncthreads();
+        for (int i = tid; i < groups; i += KVP_THREADS)
+            s_xv[i] = s_xv[i] == INFINITY ? low : s_xv[i];
+        __syncthreads();
+    }
     for (; kb < k1; kb += KVP_WARPS * KVP_STEP) {
         const bool more = kb + KVP_WARPS * KVP_STEP < k1;
         float s[2][NT][4];

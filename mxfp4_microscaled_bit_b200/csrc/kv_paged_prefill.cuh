@@ -44,6 +44,7 @@ constexpr int KPP_SLOTS = 4;           // blocks whose page factors are held at 
 constexpr int KPP_MIN_BLOCKS = 4;      // blocks of keys to a CTA, at least (one request of 512 rows over 4096
                                        // keys: 2 / 3 / 4 / 8 / 16 take 38 / 34 / 36 / 43 / 61 us)
 constexpr int KPP_LAZY = 8;            // log2 growth of the maximum that is let pass
+constexpr int KPP_SCAN = 1 << 20;      // pages among which a page of zeros looks for others (a wait ends in 1 s)
 constexpr int KPP_BIAS = KVP_BIAS - KPP_LAZY;  // how far below the maximum M is put
 
 struct KppCtrl {
@@ -593,14 +594,32 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         int page = page_of(0);
         uint32_t kbyte = page >= 0 ? a.ks[(int64_t)page * a.H + h] : 0u;
         uint32_t vbyte = page >= 0 ? a.vs[(int64_t)page * a.H + h] : 0u;
+        // a page of zeros (kv_paged_attention.cuh): on the first one, warp 8 looks through the job's pages
+        float zero_x = INFINITY;
+        auto find_zero_x = [&]() {
+            float low = INFINITY;
+            const uint32_t end = min(kend, key0 + blocks * KPP_KEYS);
+            uint32_t key = key0 + (lane << a.shift);  // may pass 2^31 behind the end
+#pragma unroll 4
+            for (int n = 0; n < KPP_SCAN / 32; ++n, key += 32 << a.shift) {
+                if (key >= end)
+                    break;
+                const int p = table[key >> a.shift];
+                const uint32_t byte = p >= 0 && p < a.NP ? a.vs[(int64_t)p * a.H + h] : 0u;
+                low = byte ? fminf(low, (float)((int)byte - 127)) : low;
+            }
+            return kvp_zero_exponent(warp_min(low));
+        };
         for (int i = 0; i < blocks; ++i) {
             const int next = page_of(i + 1);
             const int st = i & 1, par = ((i >> 1) & 1) ^ 1;
+            if (warp == 8 && zero_x == INFINITY && __any_sync(0xffffffffu, page >= 0 && vbyte == 0u))
+                zero_x = find_zero_x();
             if (i >= 2 && !warp_wait(&ct.kfree[st], par, abort, lane))
                 break;
             if (scales) {
                 const int slot = i & (KPP_SLOTS - 1);
-                const float x = vbyte ? (float)((int)vbyte - 127) : KVP_ZERO_X;
+                const float x = vbyte ? (float)((int)vbyte - 127) : zero_x;
                 ct.kf[slot][lane] = mxfp8_scale(kbyte);
                 ct.xv[slot][lane] = page >= 0 ? x : -INFINITY;
                 ct.c[slot][lane] = page >= 0 ? ex2(-x) * pow2_const(-KPP_BIAS) : 0.0f;

@@ -85,7 +85,7 @@ def sink(q, caches, table, P, G, D, row, gap, whole_page):
         vc[page], vb[page] = 0, 0
 
 
-@pytest.mark.parametrize("whole_page", [False])
+@pytest.mark.parametrize("whole_page", [False, True])
 @pytest.mark.parametrize("D,G,P,L,new,gap", [
     (128, 4, 16, 4000, 1, 20.0),    # the split kernel, its splits joined in a cluster
     (64, 4, 64, 20000, 1, 20.0),    # and through the workspace
@@ -109,3 +109,28 @@ def test_attention_of_scores_whose_rounding_passes_the_weights_room(new, big):
     status_ok()
     held = np.nan_to_num(np.abs(ref.cache_values(vc, vb))).max()
     assert bool(out.isfinite().all()) and float(out.abs().max()) <= held * (1 + 2 * BF16)
+
+
+@pytest.mark.parametrize("v_shift", [-30, -60, 40])
+@pytest.mark.parametrize("L,new,zero", [
+    (170, 1, [1, 4]), (170, 70, [1, 4]), (90, 5, [0]), (90, 90, [0]),
+    (3000, 1, list(range(40))), (3000, 60, list(range(40))),  # whole splits, and shared parts, of zero pages
+    (3000, 1, list(range(100, 188))), (700, 33, [44, 45]),    # the last ones, which some rows see in part
+    (25000, 1, list(range(3, 1500)))])
+def test_attention_zero_pages_beside_values_of_any_magnitude(L, new, zero, v_shift):
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(1, 1, 4, 64, 16, [L], [new], seed=L + new)
+    vb = (vb.astype(int) + v_shift).astype(np.uint8)
+    vc[table[0, zero]], vb[table[0, zero]] = 0, 0
+    range_check(q, ((kc, kb), (vc, vb)), table, lens, cu, 16)
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_attention_zero_pages_between_pages_far_apart(new):
+    """The zero pages come before the pages of the smallest values, and after."""
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(2, 2, 4, 128, 16, [600, 300], [new, new], seed=2, sigma=0.5)
+    vb = vb.astype(int)
+    for b in range(2):
+        vb[table[b, 8:]] -= 22
+        for p in (1, 12):
+            vc[table[b, p]], vb[table[b, p]] = 0, 0
+    range_check(q, ((kc, kb), (vc, vb.astype(np.uint8))), table, lens, cu, 16)
