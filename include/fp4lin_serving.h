@@ -15,7 +15,7 @@
  * The 8-bit format ("MXFP8" below): E4M3 elements under one power-of-two scale
  * per block, an E8M0 byte.  For a block whose largest FINITE magnitude is amax,
  * X is the least integer >= -126 with amax <= 448 * 2^X, the byte is X + 127
- * (0 when amax = 0) and each code is E4M3 round-to-nearest-even of v * 2^-X, so
+ * (0 for a block of zeros) and each code is E4M3 round-to-nearest-even of v * 2^-X, so
  * no finite value saturates; infinities saturate to +-448 * 2^X, NaN stays NaN.
  * The value is code * 2^(byte - 127).
  *

@@ -178,14 +178,14 @@ struct AppendShape {
     int T, H, shift, per_cta;
 };
 
-// Largest finite magnitude of eight bf16.
+// Largest block_abs of eight bf16.
 __device__ __forceinline__ float bf16x8_amax(uint4 u)
 {
     float f[8], m = 0.0f;
     bf16x8_to_f32(u, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, finite_abs(f[i]));
+        m = fmaxf(m, block_abs(f[i]));
     return m;
 }
 

@@ -6,7 +6,8 @@
 // (the element with the largest magnitude lands in (224, 448]); byte = X + 127.  E4M3 keeps its
 // relative step over 2^15, so a power of two loses nothing against amax/448 except at the bottom
 // of that range, and re-encoding a block to a larger X is exact down to E4M3's subnormals.
-// Byte 0 is kept for blocks whose maximum is 0: all their codes are zero.
+// Byte 0 is kept for blocks of zeros: all their codes are zero.  (Infinities and NaN leave the maximum
+// alone, but a block of nothing else gets byte 1, so that a reader may pass over byte 0.)
 #pragma once
 
 #include "common.cuh"
@@ -56,7 +57,7 @@ __device__ __forceinline__ void ld_nc_32B_if(const void *p, bool wide, bool go, 
     }
 }
 
-// E8M0 byte of a block whose largest finite magnitude is amax (amax >= 0, finite).
+// E8M0 byte of a block whose largest block_abs is amax.
 __device__ __forceinline__ uint32_t mxfp8_scale_byte(float amax)
 {
     const uint32_t u = __float_as_uint(amax);
@@ -78,11 +79,18 @@ __device__ __forceinline__ float mxfp8_scale(uint32_t byte)
     return __uint_as_float(byte ? byte << 23 : 0x400000u);
 }
 
-// |v| where v is finite, else 0: one infinity or NaN does not spoil its block's scale.
+// |v| where v is finite, else 0.
 __device__ __forceinline__ float finite_abs(float v)
 {
     const float a = fabsf(v);
     return a <= 3.402823466e38f ? a : 0.0f;
+}
+
+// A value's part in its block's amax: |v|, and the least magnitude there is for an infinity or NaN.
+__device__ __forceinline__ float block_abs(float v)
+{
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? a : __uint_as_float(1u);
 }
 
 // f16x2 of two floats, in one instruction (a conversion of one float takes the slow unit).

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(THREADS) rmsnorm_mxfp8_kernel(NormShape a)
             float amax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                amax = fmaxf(amax, finite_abs(v[i]));
+                amax = fmaxf(amax, block_abs(v[i]));
             byte = mxfp8_scale_byte(amax);
             const float inv = mxfp8_inverse(byte);
             uint32_t c[8];

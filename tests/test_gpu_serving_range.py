@@ -134,3 +134,50 @@ def test_attention_zero_pages_between_pages_far_apart(new):
         for p in (1, 12):
             vc[table[b, p]], vb[table[b, p]] = 0, 0
     range_check(q, ((kc, kb), (vc, vb.astype(np.uint8))), table, lens, cu, 16)
+
+
+# ------------------------------------------------------------------ blocks of nothing finite
+@pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
+def test_append_and_attention_of_pages_without_a_finite_value(what):
+    """Infinities saturate at 448 times the least scale there is, and shrink to nothing when the
+    page's scale grows; a page of them, or of NaN, is not taken for one of zeros."""
+    H, P, D = 2, 16, 64
+    caches = [(torch.full((2, H, P, D), 0x55, dtype=torch.uint8, device=DEV),
+               torch.full((2, H), 9, dtype=torch.uint8, device=DEV)) for _ in range(2)]
+    x = torch.zeros(1, H, D, dtype=torch.bfloat16, device=DEV)
+    x[:, :, ::3] = what
+    k = torch.zeros_like(x)
+    fl.kv_fp8_store(k, x, gpu([16]), *caches)
+    status_ok()
+    codes, byte = caches[1][0][1, :, 0].cpu(), caches[1][1][1].cpu()
+    bad = 0x7F if what != what else 0x7E if what > 0 else 0xFE
+    assert (byte == 1).all() and not codes[:, 1::3].any()
+    assert ((codes[:, ::3] & 0x7F) == 0x7F).all() if what != what else (codes[:, ::3] == bad).all()
+    assert not caches[0][1][1].any() and not caches[0][0][1, :, 0].any()  # zeros: byte 0
+    for new in (1, 40):  # one row of keys, seen by one token or by the first of many
+        q = torch.ones(new, 2 * H, D, dtype=torch.bfloat16, device=DEV)
+        out = fl.kv_fp8_attention(q, *caches, gpu([[1, 0, 0, 0]]), gpu([0]), gpu([0, new]), max_new=new, max_len=64)[0]
+        status_ok()
+        want = 448.0 * 2.0 ** -126 * (1 if what > 0 else -1)
+        got = ref.f64(out)
+        assert np.isnan(got[:, ::3]).all() if what != what else (np.abs(got[:, ::3] - want) <= BF16 * abs(want)).all()
+        assert not got[:, 1::3].any()
+    y = torch.randn(1, H, D, device=DEV).to(torch.bfloat16)
+    fl.kv_fp8_store(k, y, gpu([17]), *caches)
+    status_ok()
+    codes, byte = caches[1][0][1, :, 0].cpu(), caches[1][1][1].cpu()
+    assert byte.tolist() == ref.block_byte(np.abs(ref.f64(y))[0].max(1)).tolist()
+    assert ((codes[:, ::3] & 0x7F) == 0x7F).all() if what != what else not (codes & 0x7F).any()
+
+
+def test_norm_of_a_block_without_a_finite_value():
+    x = torch.randn(3, 128, device=DEV).abs().to(torch.bfloat16) + 1
+    x[2, 96:] = 0
+    w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    w[32:64] = float("inf")
+    w[64:96] = float("nan")
+    c, s, _ = fl.rmsnorm_mxfp8(x, w)
+    status_ok()
+    byte = ref.tc_rows(s.cpu().numpy(), 3, 4)
+    assert (byte[:, 1:3] == 1).all() and (c[:, 32:64] == 0x7E).all() and (c[:, 64:96] & 127 == 127).all()
+    assert byte[2, 3] == 0 and not c[2, 96:].any() and (byte[:, 0] > 1).all()
