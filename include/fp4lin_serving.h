@@ -70,7 +70,9 @@ int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_
  *     on the way in, for weights quantised with that rotation; 0 does not.
  *   x_scales given: x is MXFP8, E4M3 bytes [M, K] with row stride ld_x (a
  *     multiple of 16) and x_scales the tensor-core layout of [M, K/32];
- *     hadamard must be 0 (rmsnorm_mxfp8 rotates what it writes).
+ *     hadamard must be 0 (rmsnorm_mxfp8 rotates what it writes).  Blocks whose
+ *     scale is more than 2^21 below the largest of their row in 256 values are
+ *     rounded, to 2^-31 of that scale at most.
  *   w_codes [N, K/2]; w_scales tensor-core layout of [N, K/16] (NVFP4) or
  *     [N, K/32] (MXFP4); g_w device float (NVFP4);
  *   y: bf16 [M, N], row stride ldy >= N (any).

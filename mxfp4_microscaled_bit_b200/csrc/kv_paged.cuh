@@ -199,10 +199,10 @@ __device__ __forceinline__ uint2 bf16x8_encode(uint4 u, float inv)
     return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
-// f16x2 of 2^-k for k >= 0 (0 from k = 25 on: E4M3 codes times that are all below half a step).
-__device__ __forceinline__ uint32_t f16x2_pow2_neg(int k)
+// f16x2 of 2^k for k <= 15 (0 below f16's least, 2^-24).
+__device__ __forceinline__ uint32_t f16x2_pow2(int k)
 {
-    const uint32_t h = k <= 14 ? (uint32_t)(15 - k) << 10 : k <= 24 ? 1u << (24 - k) : 0u;
+    const uint32_t h = k >= -14 ? (uint32_t)(15 + k) << 10 : k >= -24 ? 1u << (24 + k) : 0u;
     return h | (h << 16);
 }
 
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(APPEND_THREADS, 3) kv_append_kernel(AppendShap
             for (int r = r0; r < min(r0 + 16, n); r += RPW)
                 *reinterpret_cast<uint2 *>(dst + (off + r) * D) = bf16x8_encode(ld_nc_v4(src + (int64_t)r * ld), inv);
         if (off && byte > old && old) {  // older rows (all zero codes under byte 0) to the larger exponent
-            const uint32_t f = f16x2_pow2_neg((int)(byte - old));
+            const uint32_t f = f16x2_pow2((int)(old - byte));  // 0: codes times that are below half an E4M3 step
             for (int r = in_group * RPW + sub; r < off; r += warps * RPW) {
                 uint2 *c = reinterpret_cast<uint2 *>(dst + r * D);
                 const uint2 v = *c;

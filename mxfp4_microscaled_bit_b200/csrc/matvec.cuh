@@ -8,8 +8,13 @@
 // goes from a 256-bit load to a tensor-core fragment in registers: E2M1 times its scale is exact
 // in f16 (at most 6 bits), so the scale costs one f16x2 multiply a pair and the product accumulates
 // in binary32 over the whole slice of K.  Exponents that f16 cannot hold are taken out first:
-//   x: scaled by a power of two (a row's largest magnitude in 256 values lands in [2^14, 2^15));
-//      what is below 2^-39 of that maximum is lost, less than binary32 sums resolve;
+//   x, bf16: scaled by a power of two (a row's largest magnitude in 256 values lands in [2^14, 2^15));
+//      what is below 2^-39 of that maximum is lost, less than binary32 sums resolve where that value
+//      meets a weight;
+//   x, MXFP8: the row's largest scale in 256 values becomes 2^MV_X8_TOP, so that codes reach 28672.
+//      Exact for blocks whose scale is down to 2^-21 of it, the others are rounded to 2^-30 of it (with
+//      the largest at 1, codes of a block 2^16 below it lost bits and from 2^25 on all of them, which is
+//      the whole answer where the larger block meets zero weights);
 //   MXFP4 scales: relative to the row's largest in 256 values; blocks more than 2^24 below it lose
 //      bits that the sum could not hold either.
 // Rotated activations are rounded to f16 once (2^-11 relative steps, against bf16 outputs).
@@ -27,7 +32,7 @@
 #include <cooperative_groups.h>
 
 #include "kv_attention.cuh"  // mma_16816x
-#include "kv_paged.cuh"      // f16x2_pow2_neg
+#include "kv_paged.cuh"      // f16x2_pow2
 #include "mxfp8.cuh"
 #include "quantize.cuh"
 
@@ -40,6 +45,7 @@ constexpr int MV_CHUNK = 256;      // k a warp step: 64 consecutive values a lan
 constexpr int MV_SEG = 8;          // chunks of x that a CTA holds at a time
 constexpr int MV_DEPTH = 2;        // chunks of weights that a warp has in flight
 constexpr int MV_MAX_M = 16;
+constexpr int MV_X8_TOP = 6;       // log2 of the largest MXFP8 scale in f16: 448 times that is below 2^15
 
 struct MatvecShape {
     const void *x;                 // bf16 [M, K] or E4M3 [M, K]
@@ -104,19 +110,27 @@ __device__ __forceinline__ float mv_inverse(uint32_t top) { return __uint_as_flo
 __device__ __forceinline__ float mv_scale(uint32_t top) { return __uint_as_float((mv_exponent(top) - 14u) << 23); }
 
 // A (row, chunk) of x, 8 values a lane, as f16 fragments (f) under one power of two (returned).  The
-// whole warp calls it.  MXFP8: the codes, exact in f16, relative to the chunk's largest scale.
+// whole warp calls it.  MXFP8: the codes relative to the chunk's largest scale.
 // bf16: relative to the largest magnitude, rotated first where asked (a rotation's block is 2 or 4
 // lanes' values).
 template <bool X8, int HAD>
 __device__ __forceinline__ float mv_stage(const MvRaw &r, int lane, uint4 &f)
 {
     if constexpr (X8) {
-        const uint32_t ref = __reduce_max_sync(0xffffffffu, r.byte), s = f16x2_pow2_neg((int)(ref - r.byte));
+        const uint32_t ref = __reduce_max_sync(0xffffffffu, r.byte);
+        // two factors: the first leaves every code exact (2^-9 * 2^-14 is a subnormal f16), the second,
+        // where the block is further down, rounds once
+        const int k = (int)(ref - r.byte), near = min(k, MV_X8_TOP + 14);
+        const uint32_t s = f16x2_pow2(MV_X8_TOP - near);
         uint32_t h[4];
         e4m3x4_to_f16(r.v.x, h[0], h[1]);
         e4m3x4_to_f16(r.v.y, h[2], h[3]);
         f = make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));
-        return mxfp8_scale(ref);
+        if (k > near) {
+            const uint32_t s2 = f16x2_pow2(near - k);
+            f = make_uint4(mul_f16x2(f.x, s2), mul_f16x2(f.y, s2), mul_f16x2(f.z, s2), mul_f16x2(f.w, s2));
+        }
+        return mxfp8_scale(ref) * (1.0f / (1 << MV_X8_TOP));
     } else {
         float v[8];
         bf16x8_to_f32(r.v, v);
@@ -299,10 +313,10 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                     refA = max(refA, __shfl_xor_sync(0xffffffffu, refA, o));
                     refB = max(refB, __shfl_xor_sync(0xffffffffu, refB, o));
                 }
-                sA[0] = sA[1] = f16x2_pow2_neg((int)(refA - a0));
-                sA[2] = sA[3] = f16x2_pow2_neg((int)(refA - a1));
-                sB[0] = sB[1] = f16x2_pow2_neg((int)(refB - b0));
-                sB[2] = sB[3] = f16x2_pow2_neg((int)(refB - b1));
+                sA[0] = sA[1] = f16x2_pow2((int)(a0 - refA));
+                sA[2] = sA[3] = f16x2_pow2((int)(a1 - refA));
+                sB[0] = sB[1] = f16x2_pow2((int)(b0 - refB));
+                sB[2] = sB[3] = f16x2_pow2((int)(b1 - refB));
                 fA = mxfp8_scale(refA);
                 fB = mxfp8_scale(refB);
             }

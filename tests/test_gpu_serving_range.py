@@ -181,3 +181,45 @@ def test_norm_of_a_block_without_a_finite_value():
     byte = ref.tc_rows(s.cpu().numpy(), 3, 4)
     assert (byte[:, 1:3] == 1).all() and (c[:, 32:64] == 0x7E).all() and (c[:, 64:96] & 127 == 127).all()
     assert byte[2, 3] == 0 and not c[2, 96:].any() and (byte[:, 0] > 1).all()
+
+
+# ------------------------------------------------------------------ matvec
+def scale_layout(byte):
+    """[rows, cols] scale bytes in the tensor-core layout."""
+    rows, cols = byte.shape
+    katoms = -(-cols // 4)
+    flat = np.zeros(fl.scale_bytes(rows, cols), np.uint8)
+    r, c = np.arange(rows)[:, None], np.arange(cols)[None]
+    flat[((r // 128) * katoms + c // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + c % 4] = byte
+    return flat
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,low,high", [(1, 16, 21), (5, 16, 30), (16, 25, 36), (3, 0, 60)])
+def test_matvec_of_8_bit_rows_whose_block_scales_lie_far_apart(fmt, M, low, high):
+    """The largest block of 256 values meets zero weights: the answer is the others'."""
+    N, K = 40, 768
+    rng = np.random.default_rng(M + high)
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    x = rng.integers(0, 256, (M, K), dtype=np.uint8)
+    x[(x & 127) == 127] = 1
+    byte = 150 - rng.integers(low, high + 1, (M, K // 32))
+    for chunk in range(3):
+        block = 8 * chunk + [0, 5, 7][chunk]
+        byte[:, block] = 150
+        codes[:, block * 16:block * 16 + 16] = 0
+    if fmt == "nvfp4":
+        sb, g = rng.integers(40, 100, (N, K // 16)), torch.tensor([0.25], device=DEV)
+        y = fl.nvfp4_matvec(u8(x), u8(codes), u8(scale_layout(sb)), g, x_scales=u8(scale_layout(byte)))
+    else:
+        sb = rng.integers(115, 122, (N, K // 32))
+        y = fl.mxfp4_matvec(u8(x), u8(codes), u8(scale_layout(sb)), x_scales=u8(scale_layout(byte)))
+    status_ok()
+    W = np.abs(ref.weight(codes, scale_layout(sb), fmt, 0.25))
+    xv = ref.E4M3[x] * np.repeat(2.0 ** (byte - 127.0), 32, 1)
+    want, mag = xv @ ref.weight(codes, scale_layout(sb), fmt, 0.25).T, np.abs(xv) @ W.T
+    # exact to 2^-21 of the largest scale; else rounded to f16 subnormals, half a step of which is
+    # 2^-31 of that scale
+    err = np.where(150 - byte <= 21, 0.0, 2.0 ** (150 - 127 - 31)).repeat(32, 1) @ W.T
+    tol = (K + 8) * F32 * mag + err
+    within(ref.f64(y), want, tol * (1 + BF16) + BF16 * np.abs(want), "8-bit rows")
