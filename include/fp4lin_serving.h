@@ -77,8 +77,8 @@ int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_
  *     [N, K/32] (MXFP4); g_w device float (NVFP4);
  *   y: bf16 [M, N], row stride ldy >= N (any).
  * K a multiple of 64, at most 2^24; N any, at most 2^27.  x, x_scales, w_codes,
- * w_scales 16-byte aligned.  MXFP4 block scales more than 2^24 below the
- * largest of their row in 2048 values lose bits (below the sum's resolution).
+ * w_scales 16-byte aligned.  MXFP4 blocks whose scale is 2^37 below the largest of
+ * their row in 256 values lose bits, from 2^38 on they count as zero.
  */
 int nvfp4_matvec(const void *x, const uint8_t *x_scales, int64_t M, int64_t K, int64_t ld_x,
                  int hadamard, const uint8_t *w_codes, const uint8_t *w_scales, const float *g_w,

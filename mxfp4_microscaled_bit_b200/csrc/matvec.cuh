@@ -15,8 +15,9 @@
 //      Exact for blocks whose scale is down to 2^-21 of it, the others are rounded to 2^-30 of it (with
 //      the largest at 1, codes of a block 2^16 below it lost bits and from 2^25 on all of them, which is
 //      the whole answer where the larger block meets zero weights);
-//   MXFP4 scales: relative to the row's largest in 256 values; blocks more than 2^24 below it lose
-//      bits that the sum could not hold either.
+//   MXFP4 scales: the row's largest in 256 values becomes 2^MV_W4_TOP, so that weights reach 49152.  Exact
+//      for blocks whose scale is down to 2^-36 of it, rounded at 2^-37, zero below (with the largest at 1
+//      blocks 2^24 below it lost bits, all there is where x is zero under the larger one).
 // Rotated activations are rounded to f16 once (2^-11 relative steps, against bf16 outputs).
 //
 // What it takes to come near HBM's rate with so few bytes is little to wait for before the weights are
@@ -46,6 +47,7 @@ constexpr int MV_SEG = 8;          // chunks of x that a CTA holds at a time
 constexpr int MV_DEPTH = 2;        // chunks of weights that a warp has in flight
 constexpr int MV_MAX_M = 16;
 constexpr int MV_X8_TOP = 6;       // log2 of the largest MXFP8 scale in f16: 448 times that is below 2^15
+constexpr int MV_W4_TOP = 13;      // of the largest MXFP4 scale: 6 times that is below 2^16
 
 struct MatvecShape {
     const void *x;                 // bf16 [M, K] or E4M3 [M, K]
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                         const float scale = mv_stage<X8, HAD>(raw[b], lane, f);
                         to[cb * 32 * ms] = f;
                         if (lane == 0)
-                            s_xs[cb * MV_MAX_M + m] = scale;
+                            s_xs[cb * MV_MAX_M + m] = NV ? scale : scale * (1.0f / (1 << MV_W4_TOP));
                     }
                 }
             }
@@ -313,10 +315,10 @@ __global__ void __launch_bounds__(MV_THREADS, 2) matvec_kernel(MatvecShape a)
                     refA = max(refA, __shfl_xor_sync(0xffffffffu, refA, o));
                     refB = max(refB, __shfl_xor_sync(0xffffffffu, refB, o));
                 }
-                sA[0] = sA[1] = f16x2_pow2((int)(a0 - refA));
-                sA[2] = sA[3] = f16x2_pow2((int)(a1 - refA));
-                sB[0] = sB[1] = f16x2_pow2((int)(b0 - refB));
-                sB[2] = sB[3] = f16x2_pow2((int)(b1 - refB));
+                sA[0] = sA[1] = f16x2_pow2(MV_W4_TOP + (int)(a0 - refA));
+                sA[2] = sA[3] = f16x2_pow2(MV_W4_TOP + (int)(a1 - refA));
+                sB[0] = sB[1] = f16x2_pow2(MV_W4_TOP + (int)(b0 - refB));
+                sB[2] = sB[3] = f16x2_pow2(MV_W4_TOP + (int)(b1 - refB));
                 fA = mxfp8_scale(refA);
                 fB = mxfp8_scale(refB);
             }

@@ -223,3 +223,34 @@ def test_matvec_of_8_bit_rows_whose_block_scales_lie_far_apart(fmt, M, low, high
     err = np.where(150 - byte <= 21, 0.0, 2.0 ** (150 - 127 - 31)).repeat(32, 1) @ W.T
     tol = (K + 8) * F32 * mag + err
     within(ref.f64(y), want, tol * (1 + BF16) + BF16 * np.abs(want), "8-bit rows")
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("M,low,high", [(1, 20, 36), (4, 24, 36), (11, 0, 36), (16, 30, 36), (2, 36, 45)])
+def test_matvec_of_mxfp4_weights_whose_block_scales_lie_far_apart(M, low, high, x8):
+    """x is zero in the largest block of 256 values: the answer is the others'."""
+    N, K = 150, 512
+    rng = np.random.default_rng(M + high)
+    codes = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    byte = 140 - rng.integers(low, high + 1, (N, K // 32))
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+    for block in (3, 15):
+        byte[:, block] = 140
+        x[:, block * 32:block * 32 + 32] = 0
+    if x8:
+        xc = ref.e4m3_bytes(ref.f64(x))
+        xb = np.full((M, K // 32), 127)
+        xv = ref.E4M3[xc]
+        y = fl.mxfp4_matvec(u8(xc), u8(codes), u8(scale_layout(byte)), x_scales=u8(scale_layout(xb)))
+    else:
+        xv = ref.f64(x)
+        y = fl.mxfp4_matvec(x.to(DEV), u8(codes), u8(scale_layout(byte)))
+    status_ok()
+    W = ref.weight(codes, scale_layout(byte), "mxfp4")
+    want, mag = xv @ W.T, np.abs(xv) @ np.abs(W).T
+    # exact to 2^-36 of the row's largest scale in 256 values, at 2^-37 within half a step of a subnormal
+    # f16 under 2^13, 2^-38 of that scale, and nothing is kept of 6 times the scale below
+    k = 140 - byte
+    far = np.where(k <= 36, 0.0, np.where(k == 37, 2.0 ** -38, 6.0 * 2.0 ** -k))
+    tol = (K + 8) * F32 * mag + np.abs(xv) @ (2.0 ** 13 * far).repeat(32, 1).T
+    within(ref.f64(y), want, tol * (1 + BF16) + BF16 * np.abs(want), "far MXFP4 scales")
