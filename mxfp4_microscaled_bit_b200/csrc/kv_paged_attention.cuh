@@ -12,7 +12,8 @@
 // exponent.  Its keys should not move M, nor vanish beside it: it gets KVP_ZERO_GAP less than the least
 // of a CTA's other pages.  (A constant, -8, put M 2^29 above pages of values near 2^-37.)
 // Scores, maxima, sums and outputs are binary32.  K and V codes are exact in f16; q is scaled by a
-// power of two to [1, 2) at its row's maximum (exact down to 2^-14 of it).  The weights that meet
+// power of two to [2^14, 2^15) at its row's maximum, and what is below 2^-28 of it loses bits (below 2^-14
+// with the maximum at 1, where a channel that no key uses could spoil the others).  The weights that meet
 // the value codes are rounded to f16: to 2^-11 of themselves against bf16 outputs, and below f16's
 // normals to half its smallest step, 2^-25.  So they are kept high in f16, at most 2^KVP_BIAS and a
 // binade or two above where scores pass 2^23: M is held that far below the maximum, and the split kernel
@@ -115,8 +116,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v)
     return r;
 }
 
+// The exponent byte of a row of q's maximum, kept where the power of two that takes it to [2^14, 2^15) and
+// its inverse are both normal.
+__device__ __forceinline__ uint32_t kvp_q_exponent(float m) { return m > 0.0f ? min(max(__float_as_uint(m) >> 23, 15u), 253u) : 141u; }
+__device__ __forceinline__ float kvp_q_inverse(uint32_t e) { return __uint_as_float((268u - e) << 23); }
+__device__ __forceinline__ float kvp_q_scale(uint32_t e) { return __uint_as_float((e - 14u) << 23); }
+
 // Row `rho` of a tile as f16 B fragments: this lane's D/4 values (d = t*D/4 ..) in the order the
-// key codes are used, scaled by 2^-e with e the row's largest exponent.  Returns 2^e (0 rows: 1).
+// key codes are used, under kvp_q_exponent's power of two.  Returns its inverse.
 template <int D>
 __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, uint32_t (*qb)[2])
 {
@@ -133,9 +140,8 @@ __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, u
     }
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // exponent byte of m, kept where both 2^e and 2^-e are normal
-    const uint32_t e = m > 0.0f ? min(max(__float_as_uint(m) >> 23, 1u), 253u) : 127u;
-    const float inv = __uint_as_float((254u - e) << 23);
+    const uint32_t e = kvp_q_exponent(m);
+    const float inv = kvp_q_inverse(e);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
         float f[8];
@@ -145,7 +151,7 @@ __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, u
         qb[2 * i + 1][0] = cvt_f16x2(f[4] * inv, f[5] * inv);
         qb[2 * i + 1][1] = cvt_f16x2(f[6] * inv, f[7] * inv);
     }
-    return __uint_as_float(e << 23);
+    return kvp_q_scale(e);
 }
 
 // Split form: CTA (s, b*H + h, z) takes keys [s*chunk, (s+1)*chunk) for rows z*8*NT .. of the

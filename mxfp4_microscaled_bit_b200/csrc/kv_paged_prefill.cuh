@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // q: a thread's own row, to f16 at [1, 2) times its code, into the operand layout
+    // q: a thread's own row, to f16 (kv_paged_attention.cuh), into the operand layout
     float qs = 0.0f;
     const int tile = warp >> 2, trow = tid & 127;
     const int rho = row0 + tid, tok = rho / a.G, head = rho - tok * a.G;
@@ -388,10 +388,10 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
             for (int j = 0; j < 8; ++j)
                 m = fmaxf(m, finite_abs(f[j]));
         }
-        const uint32_t e = m > 0.0f ? min(max(__float_as_uint(m) >> 23, 1u), 253u) : 127u;
+        const uint32_t e = kvp_q_exponent(m);
         // a negative scale turns q around, so that the row's factor is not negative
-        const float inv = copysignf(__uint_as_float((254u - e) << 23), a.qscale);
-        qs = __uint_as_float(e << 23) * fabsf(a.qscale);
+        const float inv = copysignf(kvp_q_inverse(e), a.qscale);
+        qs = kvp_q_scale(e) * fabsf(a.qscale);
         for (int i = 0; i < D / 8; ++i) {
             float f[8];
             bf16x8_to_f32(mine ? ld_nc_v4(src + 8 * i) : make_uint4(0u, 0u, 0u, 0u), f);

@@ -136,6 +136,17 @@ def test_attention_zero_pages_between_pages_far_apart(new):
     range_check(q, ((kc, kb), (vc, vb.astype(np.uint8))), table, lens, cu, 16)
 
 
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("far", [2.0 ** 12, 2.0 ** 20, 2.0 ** -20])
+def test_attention_of_a_query_whose_channels_are_far_apart(new, far):
+    """One channel of q away from the others, where the keys have nothing (or everything) in it."""
+    q, ((kc, kb), (vc, vb)), table, lens, cu = attention_case(1, 2, 4, 64, 32, [200], [new], seed=8)
+    q[:, :, 0] = far
+    if far > 1:
+        kc[:, :, :, 0] = 0
+    range_check(q, ((kc, kb), (vc, vb)), table, lens, cu, 32)
+
+
 # ------------------------------------------------------------------ blocks of nothing finite
 @pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
 def test_append_and_attention_of_pages_without_a_finite_value(what):
