@@ -613,10 +613,10 @@ __global__ void __launch_bounds__(KPP_THREADS, 1) kv_paged_prefill_kernel(KvPage
         for (int i = 0; i < blocks; ++i) {
             const int next = page_of(i + 1);
             const int st = i & 1, par = ((i >> 1) & 1) ^ 1;
-            if (warp == 8 && zero_x == INFINITY && __any_sync(0xffffffffu, page >= 0 && vbyte == 0u))
-                zero_x = find_zero_x();
             if (i >= 2 && !warp_wait(&ct.kfree[st], par, abort, lane))
                 break;
+            if (warp == 8 && zero_x == INFINITY && __any_sync(0xffffffffu, page >= 0 && vbyte == 0u))
+                zero_x = find_zero_x();
             if (scales) {
                 const int slot = i & (KPP_SLOTS - 1);
                 const float x = vbyte ? (float)((int)vbyte - 127) : zero_x;
