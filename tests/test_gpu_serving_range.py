@@ -265,3 +265,20 @@ def test_matvec_of_mxfp4_weights_whose_block_scales_lie_far_apart(M, low, high, 
     far = np.where(k <= 36, 0.0, np.where(k == 37, 2.0 ** -38, 6.0 * 2.0 ** -k))
     tol = (K + 8) * F32 * mag + np.abs(xv) @ (2.0 ** 13 * far).repeat(32, 1).T
     within(ref.f64(y), want, tol * (1 + BF16) + BF16 * np.abs(want), "far MXFP4 scales")
+
+
+# ------------------------------------------------------------------ tensors that lie between one another
+def test_norm_of_column_slices_of_one_buffer():
+    """x, the residual and the sum side by side in the rows of one projection's output."""
+    rows, cols = 70, 256
+    base = torch.randn(rows, 3 * cols + 8, device=DEV).to(torch.bfloat16)
+    x, r, s = base[:, :cols], base[:, cols:2 * cols], base[:, 2 * cols + 8:]
+    w = torch.randn(cols, device=DEV).to(torch.bfloat16)
+    want = fl.rmsnorm_mxfp8(x.contiguous(), w, r.contiguous(), hadamard=32)
+    keep = base.clone()
+    got = fl.rmsnorm_mxfp8(x, w, r, hadamard=32, summed=s)
+    status_ok()
+    assert got[2] is s and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(base[:, :2 * cols + 8], keep[:, :2 * cols + 8])
+    with pytest.raises(ValueError, match="overlaps residual"):
+        fl.rmsnorm_mxfp8(x, w, r, summed=base[:, 2 * cols - 8:3 * cols - 8])

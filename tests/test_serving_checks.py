@@ -152,3 +152,35 @@ def test_reference_append_keeps_older_rows_within_half_a_step():
     # one rounding when written (2^-4), and one each time the exponent grew that only subnormals feel
     assert np.all(np.abs(got - rows[:, 0]) <= 2.0 ** -4 * np.abs(rows[:, 0]) + 16 * 2.0 ** -10 * top / 224)
     assert (codes[0] == 0x7F).all() and byte[0] == 9
+
+
+def test_norms_overlap_check_against_every_byte():
+    """summed may be the residual's (x's) own memory or share none of it, which rows of one stride do
+    side by side; only where the strides differ does the check go by the whole ranges."""
+    from mxfp4_microscaled_bit_b200.serving import _apart
+    rng = np.random.default_rng(0)
+
+    def touched(at, ld, rows, cols):
+        return {at + 2 * (r * ld + c) + k for r in range(rows) for c in range(cols) for k in (0, 1)}
+
+    seen = set()
+    for _ in range(3000):
+        rows, cols = int(rng.integers(1, 5)), int(rng.integers(1, 7))
+        ld, ld_s = (int(v) for v in cols + rng.integers(0, 9, 2))
+        if rng.random() < 0.7:
+            ld_s = ld
+        lo = 1000
+        s = lo + int(rng.integers(-2 * rows * (ld + 1), 2 * rows * (ld + 1)))
+        a, b = touched(s, ld_s, rows, cols), touched(lo, ld, rows, cols)
+        same = s == lo and (ld_s == ld or rows == 1)
+        try:
+            _apart("f", s, ld_s, (("x", lo, ld),), rows, cols)
+            refused = False
+        except ValueError:
+            refused = True
+        if same or not a & b:
+            assert not refused or ld_s != ld and rows > 1, (s, ld_s, ld, rows, cols)
+        else:
+            assert refused, (s, ld_s, ld, rows, cols)
+        seen.add((same, bool(a & b), refused))
+    assert seen >= {(True, True, False), (False, True, True), (False, False, False)}
