@@ -45,7 +45,8 @@ extern "C" {
  * s = bf16(x + residual); n = (s / sqrt(mean(s^2) + eps)) * weight; rotated by
  * H_b / sqrt(b) in blocks of b = hadamard along the row when b is 16 or 32
  * (0: not); encoded to MXFP8 with one scale per 32 values.  Sums and the norm
- * are binary32.
+ * are binary32, squares included: |s| below 2^55 and, with eps = 0, rows that
+ * reach 2^-55.
  *   x, residual, summed: bf16 [rows, cols], row strides ld_x, ld_r, ld_s
  *     (multiples of 8); residual and summed are both given or both NULL (then
  *     s = x); summed receives s and may be the residual's or x's own memory
@@ -63,11 +64,15 @@ int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_
 /*
  * y[M, N] = x[M, K] W[N, K]^T with W in the library's 4-bit formats, exactly as
  * nvfp4_quantize / mxfp4_quantize write them, and x in more bits than the W4A4
- * calls take: no activation is rounded to 4 bits.  1 <= M <= 16.  Result
- * bf16_round of a binary32 sum, in a fixed order (the same bits every time).
+ * calls take: no activation is rounded to 4 bits.  1 <= M <= 16; there is no
+ * form for more rows.  Result bf16_round of a binary32 sum, in a fixed order
+ * (the same bits every time), of activations held in f16 under a power of two
+ * per row and 256 values.
  *   x_scales NULL: x is bf16 [M, K], row stride ld_x (a multiple of 8);
  *     hadamard = 16 (NVFP4) or 32 (MXFP4) rotates its blocks by H_b / sqrt(b)
  *     on the way in, for weights quantised with that rotation; 0 does not.
+ *     Exact down to 2^-31 of the row's largest in 256 values, gone below 2^-39;
+ *     rotated values are rounded to f16, 2^-11 of themselves.
  *   x_scales given: x is MXFP8, E4M3 bytes [M, K] with row stride ld_x (a
  *     multiple of 16) and x_scales the tensor-core layout of [M, K/32];
  *     hadamard must be 0 (rmsnorm_mxfp8 rotates what it writes).  Blocks whose
@@ -75,7 +80,7 @@ int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_
  *     rounded, to 2^-31 of that scale at most.
  *   w_codes [N, K/2]; w_scales tensor-core layout of [N, K/16] (NVFP4) or
  *     [N, K/32] (MXFP4); g_w device float (NVFP4);
- *   y: bf16 [M, N], row stride ldy >= N (any).
+ *   y: bf16 [M, N], row stride ldy >= N (any), not overlapping any input.
  * K a multiple of 64, at most 2^24; N any, at most 2^27.  x, x_scales, w_codes,
  * w_scales 16-byte aligned.  MXFP4 blocks whose scale is 2^37 below the largest of
  * their row in 256 values lose bits, from 2^38 on they count as zero.

@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(TABLE_THREADS) kv_table_kernel(TableShape a)
 // kv_table_kernel lays them out).  A run that begins at row 0 starts its page afresh; a later one
 // finds the page's older rows under its old scale: the larger of the two exponents is the page's
 // new one, and when it grew the older rows are re-encoded to it.
-//   2 (in) + 1 (out) bytes a value, for K and V; HBM bound for prompts, latency bound for single
-// tokens.  A CTA owns the runs that begin in its `per_cta` tokens, for one head of K or of V; the
+//   2 (in) + 1 (out) bytes a value, for K and V.  Latency bound: a CTA's slots, rows and codes wait for one
+// another, and prompts' bytes take half of its time at HBM's rate.  A CTA owns the runs that begin in its `per_cta` tokens, for one head of K or of V; the
 // CTAs of a token's heads are neighbours, so that its row is read together.  A warp takes up to 16
 // rows, all loads in flight and the values in registers between the maximum and the encoding;
 // P/16 warps are a group that takes a run.  With many runs, as in decoding, each warp takes a run

@@ -4,22 +4,23 @@
 // j uses kv head j / G.  With codes k, v and page exponents Xk, Xv:
 //   s_l = scale * 2^Xk * (q . k_l),  o = sum_l softmax(s)_l * 2^Xv * v_l.
 //
-// The value scale rides in the exponent: with s'_l = log2(e) s_l + Xv(l) and M = max s',
+// The value scale rides in the exponent: with s'_l = log2(e) s_l + Xv(l) and M near max s',
 //   w_l = 2^(s'_l - M),  o = (sum_l w_l v_l) / (sum_l w_l 2^-Xv(l)),
 // so one running maximum and one exponential a score serve both sums, the weights that meet the
-// value codes are at most 1 whatever the pages' scales, and one fused multiply-add applies both
+// value codes have one bound whatever the pages' scales, and one fused multiply-add applies both
 // scales.  A page whose value byte is 0 (all codes zero) takes part in the second sum only, under any
 // exponent.  Its keys should not move M, nor vanish beside it: it gets KVP_ZERO_GAP less than the least
 // of a CTA's other pages.  (A constant, -8, put M 2^29 above pages of values near 2^-37.)
+//
 // Scores, maxima, sums and outputs are binary32.  K and V codes are exact in f16; q is scaled by a
-// power of two to [2^14, 2^15) at its row's maximum, and what is below 2^-28 of it loses bits (below 2^-14
-// with the maximum at 1, where a channel that no key uses could spoil the others).  The weights that meet
-// the value codes are rounded to f16: to 2^-11 of themselves against bf16 outputs, and below f16's
-// normals to half its smallest step, 2^-25.  So they are kept high in f16, at most 2^KVP_BIAS and a
-// binade or two above where scores pass 2^23: M is held that far below the maximum, and the split kernel
-// loses only what is 2^-39 of a row's largest (2^-25 with the largest at 1, where all keys beside one of
-// 18 more were lost).  The second sum leaves the factor out, with its 2^-Xv, so that values of any
-// magnitude keep their room in binary32; the first leaves it out at its end.
+// power of two to [2^14, 2^15) at its row's maximum, exact down to 2^-31 of it (2^-17 with the maximum at
+// 1, where a channel that no key uses could spoil the others).  The weights that meet the value codes
+// are rounded to f16: to 2^-11 of themselves against bf16 outputs, and below f16's normals to half its
+// smallest step, 2^-25.  So they are kept high in f16, at most 2^KVP_BIAS and a binade or two above where
+// scores pass 2^23: M is that far below the maximum, and the split kernel loses only what is 2^-39 of
+// a row's largest (2^-25 with the largest at 1, where all keys beside one of 18 more were lost).  The
+// second sum leaves the factor out, with its 2^-Xv, so that values of any magnitude keep their room in
+// binary32; the first leaves it out at its end.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -1,9 +1,10 @@
 // kv_paged_prefill.cuh -- kv_paged_attention.cuh's attention for requests with many new tokens: the
 // same mathematics on tcgen05.
 //
-// Bound by the tensor cores and, as closely, by the exponentials (4 D flops and one exponential a
-// score: at D = 128 a 256 x 128 block of scores takes ~2050 cycles of either; the softmax's other
-// instructions bring its warps to ~2900).  Two prompts of up to 2048 tokens behind contexts of up to
+// 4 D flops and one exponential a score: at D = 128 a 256 x 128 block of scores is ~2050 cycles of the
+// exponential unit and ~2100 of the tensor cores, and takes ~5400.  Each is busy for two fifths of the time:
+// what sets the pace is the chain from a block's keys through its scores and weights to its values, which a
+// block with one live tile takes as long for.  Two prompts of up to 2048 tokens behind contexts of up to
 // 8191, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 592 us, 910 TFLOP/s, 55% of the measured bf16
 // rate.  One CTA an SM takes 256 (token, head) rows of one kv head, as two tiles of 128: while the
 // softmax of one runs, the tensor cores work on the other, and every key block that is converted serves

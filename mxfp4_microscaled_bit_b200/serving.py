@@ -6,6 +6,10 @@ Argument marshalling only, as in the package: every tensor is checked before its
 the C ABI, and nothing falls back to PyTorch.  These calls sit in a decoding loop, where a step of
 Python costs as much as the kernel, so the checks ask each tensor only what the call depends on.
 
+Every call takes `stream=` (default: the current stream).  Outputs and workspaces that are not given are
+made in the current stream's memory, and a call on another stream then first waits for all that the
+current stream has pending; one whose outputs and workspace are all given waits for nothing.
+
 A paged cache is a pair (codes uint8 [num_pages, H, P, D], scales uint8 [num_pages, H]), one for K
 and one for V.
 """
@@ -147,9 +151,11 @@ def rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
                   summed: torch.Tensor | None = None, stream=None):
     """RMS norm of bf16 x [rows, cols] (+ residual), rotated when hadamard is 16 or 32, in MXFP8.
 
+    The output is what weight_only_linear takes for up to 16 rows.
+
     Returns (codes uint8 [rows, cols] of E4M3 bytes, scales uint8 [scale_bytes(rows, cols/32)] of
     E8M0 bytes in the tensor-core layout, s): s = bf16(x + residual), in `summed` if given (which
-    may be the residual itself), or x where there is no residual."""
+    may be the residual or x itself, or share no memory with them), or x where there is no residual."""
     fn = "rmsnorm_mxfp8"
     dev = _device(fn, "x", x)
     if x.dim() != 2:
@@ -225,7 +231,8 @@ def _matvec(fn, nv, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream):
 
 def nvfp4_matvec(x, w_codes, w_scales, g_w, *, x_scales=None, hadamard: int = 0, out=None, stream=None):
     """y [M, N] bf16 = x W^T for NVFP4 weights and M <= 16 rows of x: bf16 [M, K] (rotated on the
-    way in when hadamard = 16), or MXFP8 codes uint8 [M, K] with x_scales (rmsnorm_mxfp8)."""
+    way in when hadamard = 16), or MXFP8 codes uint8 [M, K] with x_scales (rmsnorm_mxfp8).  out must
+    not overlap the inputs."""
     return _matvec("nvfp4_matvec", True, x, w_codes, w_scales, g_w, x_scales, hadamard, out, stream)
 
 
@@ -237,7 +244,8 @@ def mxfp4_matvec(x, w_codes, w_scales, *, x_scales=None, hadamard: int = 0, out=
 def weight_only_linear(x, weight, *, x_scales=None, out=None, stream=None):
     """y = x W^T for a prepared weight (prepare_weight, prepare_weight_gptq) and M <= 16 rows whose
     activations stay in 16 bits, or in the 8 bits of rmsnorm_mxfp8 (which must have rotated them by
-    weight.hadamard).  The W4A4 counterparts are nvfp4_linear and mxfp4_linear."""
+    weight.hadamard).  More rows are refused: their products are the W4A4 ones, nvfp4_linear and
+    mxfp4_linear, of bf16 activations."""
     had = weight.hadamard if x_scales is None else 0
     if weight.fmt == "nvfp4":
         return nvfp4_matvec(x, weight.codes, weight.scales, weight.g, x_scales=x_scales, hadamard=had, out=out,
