@@ -164,8 +164,8 @@ __device__ __forceinline__ float kvp_load_q(const __nv_bfloat16 *p, bool live, u
 // bytes.  O^T += V^T w^T: the lane needs the same dimension of keys 2t, 2t+1 in one register, two
 // byte permutes of two rows' words; it takes D/8 contiguous dimensions (those of all D/16 M tiles).
 // The weights change from the score layout to B fragments by an 8 x 8 transpose in registers.
-// 32 requests of 16384 to 32768 keys, 8 kv heads of 4, D = 128 (1.52 GB): 263 to 278 us with the merge,
-// 5.5 to 5.8 TB/s, 85 to 89% of a plain copy's rate; one request of 1000 keys 7 us.
+// 32 requests of 16384 to 32768 keys, 8 kv heads of 4, D = 128 (1.52 GB): 260 to 278 us with the merge,
+// 5.5 to 5.9 TB/s, 85 to 90% of a plain copy's rate; one request of 1000 keys 6.7 us.
 template <int D, int NT>
 __global__ void __launch_bounds__(KVP_THREADS, NT == 1 ? 3 : 2) kv_paged_split_kernel(KvPagedShape a)
 {

@@ -5,7 +5,7 @@
 // exponential unit and ~2100 of the tensor cores, and takes ~5400.  Each is busy for two fifths of the time:
 // what sets the pace is the chain from a block's keys through its scores and weights to its values, which a
 // block with one live tile takes as long for.  Two prompts of up to 2048 tokens behind contexts of up to
-// 8191, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 592 us, 910 TFLOP/s, 55% of the measured bf16
+// 8191, 8 kv heads of 4 query heads, D = 128 (539 GFLOP): 593 us, 909 TFLOP/s, 55% of the measured bf16
 // rate.  One CTA an SM takes 256 (token, head) rows of one kv head, as two tiles of 128: while the
 // softmax of one runs, the tensor cores work on the other, and every key block that is converted serves
 // both.

@@ -24,10 +24,10 @@
 // asked for, and little to do for each.  A CTA takes 128 weight rows, 16 a warp, and a slice of K; the
 // CTAs that share rows form a cluster (at most 8) along K.  The partial sums of a row go to one CTA of
 // the cluster through distributed shared memory and are added in a fixed order: one launch, no
-// workspace, the same bits every time.  Between launches of a graph: NVFP4, one rotated row, 4096 x 4096
-// 5.1 us; five rows, 4096 x 14336 12.2 us (2.7 TB/s); MXFP4, sixteen 8-bit rows, 14336 x 4096 17.8 us, of which
-// ~9 us are the weights' loads alone (two chunks of each warp in flight), the rest the conversions, scales
-// and products of 16 warps an SM.
+// workspace, the same bits every time.  Between launches of a graph, weights from HBM: NVFP4,
+// one rotated row, 4096 x 4096 4.9 us; five rows, 4096 x 14336 14.0 us (2.4 TB/s); MXFP4, sixteen 8-bit rows,
+// 14336 x 4096 19.5 us, of which ~9 us are the weights' loads alone (two chunks of each warp in flight), the
+// rest the conversions, scales and products of 16 warps an SM.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -13,9 +13,12 @@ MSE-optimal scales), gemm_quant (the prefill GEMM with its output NVFP4-encoded)
 linear_decode (16 x 14336 x 4096 with the activation quantiser inside the GEMM),
 gptq (MR-GPTQ of the 14336 x 4096 weight, NVFP4, 16-wide rotation), norm_mxfp8
 (8192 x 4096 with residual and 32-wide rotation), matvec_nvfp4 (5 x 4096 x 14336,
-bf16), matvec_mxfp4 (16 x 14336 x 4096, 8-bit activations), paged_store (8 prompts
-of 2048 tokens, 8 heads of 128), paged_decode (16 sequences of 32768 tokens, 8 kv
-heads, G = 4), paged_prefill (2 x 2048 new tokens behind 8192).
+bf16), matvec_mxfp4 (16 x 14336 x 4096, 8-bit activations), matvec_nvfp4_one (1 x 4096
+x 4096, bf16, 16-wide rotation), matvec_nvfp4_x8 (16 x 14336 x 4096, 8-bit activations),
+matvec_mxfp4_bf16 (5 x 4096 x 14336, bf16), paged_store (8 prompts of 2048 tokens, 8
+heads of 128), paged_decode (16 sequences of 32768 tokens, 8 kv heads, G = 4),
+paged_draft (32 sequences of 4096 tokens, 4 new ones each), paged_few_rows (8 new ones),
+paged_prefill (2 x 2048 new tokens behind 8192).
 """
 from __future__ import annotations
 
@@ -38,7 +41,8 @@ def main():
                     choices=["gemm_prefill", "gemm_mxfp4", "gemm_decode", "quant_prefill", "quant_prefill_static",
                              "quant_prefill_static_h0", "kv_load", "kv_store", "kv_attention", "quant_mse",
                              "gemm_quant", "linear_decode", "gptq", "norm_mxfp8", "matvec_nvfp4", "matvec_mxfp4",
-                             "paged_store", "paged_decode", "paged_prefill"])
+                             "matvec_nvfp4_one", "matvec_nvfp4_x8", "matvec_mxfp4_bf16", "paged_store",
+                             "paged_decode", "paged_draft", "paged_few_rows", "paged_prefill"])
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--kv-batch", type=int, default=8,
                     help="sequences in the kv_* cases' cache (8 x 8 x 32768 x 128 by default)")
@@ -59,16 +63,19 @@ def main():
         w = si.normal_bf16(3, 1, x.shape[1]).view(-1).to(dev)
         fn = lambda: fl.rmsnorm_mxfp8(x, w, r, hadamard=32)  # noqa: E731
     elif a.case.startswith("matvec"):
-        M, N, K = (5, 4096, 14336) if a.case == "matvec_nvfp4" else (16, 14336, 4096)
-        w = fl.prepare_weight(si.decode_W(N, K).to(dev), a.case[7:], 0)
+        fmt, x8 = a.case.split("_")[1], a.case in ("matvec_mxfp4", "matvec_nvfp4_x8")
+        one = a.case == "matvec_nvfp4_one"
+        M, N, K = (16, 14336, 4096) if x8 else (1, 4096, 4096) if one else (5, 4096, 14336)
+        w = fl.prepare_weight(si.decode_W(N, K).to(dev), fmt, 16 if one else 0)
         x = si.decode_A(M, K).to(dev)
         xs = None
-        if a.case == "matvec_mxfp4":
+        if x8:
             x, xs = fl.rmsnorm_mxfp8(x, torch.ones(K, dtype=torch.bfloat16, device=dev))[:2]
         fn = lambda: fl.weight_only_linear(x, w, x_scales=xs)  # noqa: E731
     elif a.case.startswith("paged"):
         H, G, D, P = 8, 4, 128, 64
-        B, past, new = {"paged_store": (8, 0, 2048), "paged_decode": (16, 32767, 1), "paged_prefill": (2, 8192, 2048)}[a.case]
+        B, past, new = {"paged_store": (8, 0, 2048), "paged_decode": (16, 32767, 1), "paged_draft": (32, 4096, 4),
+                        "paged_few_rows": (32, 4096, 8), "paged_prefill": (2, 8192, 2048)}[a.case]
         width = -(-(past + new) // P)
         table = torch.randperm(B * width, device=dev).to(torch.int32).view(B, width)
         caches = [(torch.randint(0, 126, (B * width, H, P, D), dtype=torch.uint8, device=dev),
