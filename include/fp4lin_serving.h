@@ -54,7 +54,7 @@ extern "C" {
  *   weight: bf16 [cols]; eps >= 0;
  *   codes: [rows, cols] E4M3 bytes; scales: tensor-core layout of
  *     [rows, cols/32] E8M0 bytes, fp4lin_scale_bytes(rows, cols/32) bytes,
- *     padding written 0.
+ *     padding written 0; neither overlaps anything else.
  * cols a multiple of 32, at most 32768; pointers 16-byte aligned.
  */
 int rmsnorm_mxfp8(const void *x, int64_t ld_x, const void *residual, int64_t ld_r,
