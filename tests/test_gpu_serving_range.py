@@ -282,3 +282,57 @@ def test_norm_of_column_slices_of_one_buffer():
     assert torch.equal(base[:, :2 * cols + 8], keep[:, :2 * cols + 8])
     with pytest.raises(ValueError, match="overlaps residual"):
         fl.rmsnorm_mxfp8(x, w, r, summed=base[:, 2 * cols - 8:3 * cols - 8])
+
+
+# ------------------------------------------------------------------ offsets that pass 32 bits
+def test_paged_cache_of_more_than_4_gb():
+    """The same step on the last pages of a large cache and on a small one: the same bits."""
+    H, G, P, D, lens, new = 8, 2, 128, 128, [300, 40], [1, 30]
+    far = (1 << 32) // (H * P * D) + 1
+    g = torch.Generator(device=DEV).manual_seed(0)
+    kv = torch.randn(2, 371, H, D, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn(31, H * G, D, generator=g, device=DEV).to(torch.bfloat16)
+    outs = []
+    for first in (0, far):
+        caches = [(torch.empty((first + 4, H, P, D), dtype=torch.uint8, device=DEV),
+                   torch.empty((first + 4, H), dtype=torch.uint8, device=DEV)) for _ in range(2)]
+        for codes, scales in caches:
+            codes[first:], scales[first:] = 0, 0
+        table = gpu(np.array([[2, 0, 3], [1, -1, -1]]) + first * (np.arange(3) < [[3], [1]]))
+        p = [np.arange(n) for n in (301, 70)]
+        rows = table.cpu().numpy()
+        slots = np.concatenate([rows[b, p[b] // P] * P + p[b] % P for b in range(2)])
+        fl.kv_fp8_store(kv[0], kv[1], gpu(slots), *caches)
+        out = fl.kv_fp8_attention(q, *caches, table, gpu(lens), gpu([0, 1, 31]), max_new=30, max_len=301)
+        status_ok()
+        outs.append([out] + [t[first:].clone() for c in caches for t in c])
+        del caches
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    torch.cuda.empty_cache()
+
+
+def test_norm_and_matvec_of_more_than_4_gb():
+    rows, cols = 70000, 32768
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[-130:] = torch.randn(130, cols, device=DEV).to(torch.bfloat16)
+    w = torch.randn(cols, device=DEV).to(torch.bfloat16)
+    c, s, _ = fl.rmsnorm_mxfp8(x, w, hadamard=16)
+    status_ok()
+    cut = rows // 128 * 128 - 128  # whole tiles of the scale layout
+    c0, s0, _ = fl.rmsnorm_mxfp8(x[cut:], w, hadamard=16)
+    assert torch.equal(c[cut:], c0) and torch.equal(s[cut * cols // 32:], s0)
+    del x, c, s
+    N, K = (1 << 20) + 3, 8256
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros(fl.scale_bytes(N, K // 32), dtype=torch.uint8, device=DEV)
+    codes[-131:] = torch.randint(0, 256, (131, K // 2), device=DEV).to(torch.uint8)
+    tail = fl.scale_bytes(131, K // 32)  # the last 131 rows are two tiles
+    scales[-tail:] = torch.randint(110, 130, (tail,), device=DEV).to(torch.uint8)
+    x = torch.randn(3, K, device=DEV).to(torch.bfloat16)
+    y = fl.mxfp4_matvec(x, codes, scales)
+    status_ok()
+    assert not y[:, :-131].any()
+    W = ref.weight(codes[-131:].cpu().numpy(), scales[-tail:].cpu().numpy(), "mxfp4")
+    want, mag = ref.f64(x) @ W.T, np.abs(ref.f64(x)) @ np.abs(W).T
+    within(ref.f64(y[:, -131:]), want, (K + 8) * F32 * mag * (1 + BF16) + BF16 * np.abs(want), "the last rows")
+    torch.cuda.empty_cache()
